@@ -1,7 +1,7 @@
 """memory_bound_fk_b200 -- fused memory-bound operators for NVIDIA B200 (sm_100a).
 
-Python binding of ``libfk.so`` (declared in ``include/fk.h``).  This module
-only marshals arguments: every step of the computation runs in the
+Python binding of ``libfk.so`` (declared in ``include/fk.h`` and
+``include/fk_q8.h``).  This module only marshals arguments: every step of the computation runs in the
 library's CUDA kernels.  PyTorch provides device memory and streams.
 
 Raw C-ABI mirrors (same names, pointers as integers, stream as a
@@ -20,6 +20,14 @@ Raw C-ABI mirrors (same names, pointers as integers, stream as a
     fk_layernorm_rows_ex(x, y, gamma, beta, rows, cols, dtype, eps, epilogue, plan, stream) -> status
     fk_layernorm_rows_plan(rows, cols, dtype, path=FK_PATH_AUTO) -> SoftmaxPlan
     fk_attention_fwd(q, k, v, o, bh, t, d, causal, scale, stream) -> status
+    fk_rmsnorm_rows(x, residual, gamma, y, scales, h, rows, cols, dtype, out_dtype, eps, stream) -> status
+    fk_rmsnorm_rows_bwd(dy, h, gamma, dres, dx, dgamma, rows, cols, dtype, eps, stream) -> status
+    fk_rmsnorm_rows_bwd_workspace(rows, cols, dtype, want_dgamma) -> bytes
+    fk_rmsnorm_rows_bwd_ws(..., eps, workspace, workspace_bytes, stream) -> status
+    fk_quantize_rows(x, q, scales, rows, cols, dtype, out_dtype, epilogue, stream) -> status
+    fk_matmul_q8(a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, stream) -> status
+    fk_matmul_q8_workspace(m, n, k, aligned) -> bytes
+    fk_matmul_q8_ws(..., epilogue, workspace, workspace_bytes, stream) -> status
     fk_status_string(status) -> str
     fk_wait_timeouts(reset=False) -> int     (bounded-wait give-ups, synchronous)
     fk_wait_selftest(timeout_us, stream) -> status
@@ -31,6 +39,10 @@ Tensor conveniences (contiguous CUDA tensors; the current torch stream):
     softmax_causal(x, scale, period=None, offset=0, out=None, plan=None)
     layernorm(x, eps=1e-5, weight=None, bias=None, gelu=None, out=None, plan=None)
     attention(q, k, v, causal=True, scale=None, out=None)   # [..., t, d] bf16
+    rmsnorm(x, weight=None, eps=1e-6, residual=None, out_dtype=None, ...)   # + residual, to 8 bits or not
+    rmsnorm_backward(dy, h, weight=None, eps=1e-6, dresidual=None, ...) -> (dx, dweight)
+    quantize_rows(x, dtype=torch.int8, gelu=None, ...) -> (codes, scales)
+    matmul_q8(a, a_scales, b, b_scales, bias=None, gelu=None, out_dtype=torch.bfloat16, ...)
 
 There is no fallback: if the library is missing or a call fails, an
 exception is raised.
@@ -44,6 +56,7 @@ import re
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfk.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "fk.h")
+Q8_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "fk_q8.h")
 
 # fk_status
 FK_OK = 0
@@ -54,6 +67,9 @@ FK_ERR_CUDA = 4
 # fk_dtype
 FK_F32 = 0
 FK_BF16 = 1
+# fk_q8type
+FK_I8 = 2
+FK_E4M3 = 3
 # fk_gelu_kind
 FK_GELU_TANH = 0
 FK_GELU_ERF = 1
@@ -142,6 +158,23 @@ def lib() -> ctypes.CDLL:
         L.fk_attention_fwd.restype = ci
         L.fk_layernorm_rows_plan.argtypes = [sz, sz, ci, ci, ctypes.POINTER(SoftmaxPlan)]
         L.fk_layernorm_rows_plan.restype = ci
+        f, szp = ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+        L.fk_rmsnorm_rows.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, ci, ci, f, vp]
+        L.fk_rmsnorm_rows.restype = ci
+        L.fk_rmsnorm_rows_bwd.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, ci, f, vp]
+        L.fk_rmsnorm_rows_bwd.restype = ci
+        L.fk_rmsnorm_rows_bwd_ws.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, ci, f, vp, sz, vp]
+        L.fk_rmsnorm_rows_bwd_ws.restype = ci
+        L.fk_rmsnorm_rows_bwd_workspace.argtypes = [sz, sz, ci, ci, szp]
+        L.fk_rmsnorm_rows_bwd_workspace.restype = ci
+        L.fk_quantize_rows.argtypes = [vp, vp, vp, sz, sz, ci, ci, ci, vp]
+        L.fk_quantize_rows.restype = ci
+        L.fk_matmul_q8.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, sz, ci, ci, ci, vp]
+        L.fk_matmul_q8.restype = ci
+        L.fk_matmul_q8_ws.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, sz, ci, ci, ci, vp, sz, vp]
+        L.fk_matmul_q8_ws.restype = ci
+        L.fk_matmul_q8_workspace.argtypes = [sz, sz, sz, ci, szp]
+        L.fk_matmul_q8_workspace.restype = ci
         L.fk_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint), ci]
         L.fk_wait_timeouts.restype = ci
         L.fk_wait_selftest.argtypes = [ctypes.c_uint, vp]
@@ -151,9 +184,12 @@ def lib() -> ctypes.CDLL:
 
 
 def header_functions() -> list[str]:
-    """Names of the entry points declared in include/fk.h."""
-    text = open(HEADER_PATH).read()
-    return re.findall(r"FK_API\s+[\w\s\*]+?\b(fk_\w+)\s*\(", text)
+    """Names of the entry points declared in include/fk.h and include/fk_q8.h."""
+    names = []
+    for path in (HEADER_PATH, Q8_HEADER_PATH):
+        with open(path) as f:
+            names += re.findall(r"FK_API\s+[\w\s\*]+?\b(fk_\w+)\s*\(", f.read())
+    return names
 
 
 # ---------------------------------------------------------------- raw mirrors
@@ -237,6 +273,57 @@ def fk_layernorm_rows_plan(rows: int, cols: int, dtype: int, path: int = FK_PATH
 def fk_attention_fwd(q: int, k: int, v: int, o: int, bh: int, t: int, d: int, causal: int, scale: float,
                      stream: int = 0) -> int:
     return lib().fk_attention_fwd(q, k, v, o, bh, t, d, causal, scale, stream)
+
+
+def fk_rmsnorm_rows(x: int, residual: int, gamma: int, y: int, scales: int, h: int, rows: int, cols: int, dtype: int,
+                    out_dtype: int, eps: float, stream: int = 0) -> int:
+    return lib().fk_rmsnorm_rows(x, residual, gamma, y, scales, h, rows, cols, dtype, out_dtype, eps, stream)
+
+
+def fk_rmsnorm_rows_bwd(dy: int, h: int, gamma: int, dres: int, dx: int, dgamma: int, rows: int, cols: int,
+                        dtype: int, eps: float, stream: int = 0) -> int:
+    return lib().fk_rmsnorm_rows_bwd(dy, h, gamma, dres, dx, dgamma, rows, cols, dtype, eps, stream)
+
+
+def fk_rmsnorm_rows_bwd_workspace(rows: int, cols: int, dtype: int, want_dgamma: bool = True) -> int:
+    """Workspace bytes fk_rmsnorm_rows_bwd of this shape uses."""
+    b = ctypes.c_size_t(0)
+    st = lib().fk_rmsnorm_rows_bwd_workspace(rows, cols, dtype, int(bool(want_dgamma)), ctypes.byref(b))
+    if st != FK_OK:
+        raise FkError(st, "fk_rmsnorm_rows_bwd_workspace")
+    return b.value
+
+
+def fk_rmsnorm_rows_bwd_ws(dy: int, h: int, gamma: int, dres: int, dx: int, dgamma: int, rows: int, cols: int,
+                           dtype: int, eps: float, workspace: int, workspace_bytes: int, stream: int = 0) -> int:
+    return lib().fk_rmsnorm_rows_bwd_ws(dy, h, gamma, dres, dx, dgamma, rows, cols, dtype, eps, workspace,
+                                        workspace_bytes, stream)
+
+
+def fk_quantize_rows(x: int, q: int, scales: int, rows: int, cols: int, dtype: int, out_dtype: int,
+                     epilogue: int = FK_EPILOGUE_NONE, stream: int = 0) -> int:
+    return lib().fk_quantize_rows(x, q, scales, rows, cols, dtype, out_dtype, epilogue, stream)
+
+
+def fk_matmul_q8(a: int, b: int, a_scales: int, b_scales: int, bias: int, c: int, m: int, n: int, k: int, dtype: int,
+                 out_dtype: int, epilogue: int = FK_EPILOGUE_NONE, stream: int = 0) -> int:
+    return lib().fk_matmul_q8(a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, stream)
+
+
+def fk_matmul_q8_workspace(m: int, n: int, k: int, aligned: bool = True) -> int:
+    """Workspace bytes fk_matmul_q8 uses (aligned: a and b on 16-byte boundaries)."""
+    b = ctypes.c_size_t(0)
+    st = lib().fk_matmul_q8_workspace(m, n, k, int(bool(aligned)), ctypes.byref(b))
+    if st != FK_OK:
+        raise FkError(st, "fk_matmul_q8_workspace")
+    return b.value
+
+
+def fk_matmul_q8_ws(a: int, b: int, a_scales: int, b_scales: int, bias: int, c: int, m: int, n: int, k: int,
+                    dtype: int, out_dtype: int, epilogue: int, workspace: int, workspace_bytes: int,
+                    stream: int = 0) -> int:
+    return lib().fk_matmul_q8_ws(a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, workspace,
+                                 workspace_bytes, stream)
 
 
 def fk_status_string(status: int) -> str:
@@ -470,6 +557,194 @@ def attention(q, k, v, causal: bool = True, scale: float | None = None, out=None
     return out
 
 
+# ---------------------------------------------------------------- the 8-bit linear layer
+
+_Q8_TYPES: dict = {}    # torch.int8 / torch.float8_e4m3fn -> fk_q8type, filled at first use
+
+
+def _q8_code(dt):
+    """fk_q8type of a torch dtype, or None."""
+    if not _Q8_TYPES:
+        import torch
+        _Q8_TYPES.update({torch.int8: FK_I8, torch.float8_e4m3fn: FK_E4M3})
+    return _Q8_TYPES.get(dt)
+
+
+def _like(t, name: str, shape, dtype, device) -> int:
+    """Address of an operand that must be contiguous CUDA memory of this
+    shape, type and device (0 for None)."""
+    if t is None:
+        return 0
+    _check_tensor(t, name)
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} and type {dtype}, on {device}")
+    return t.data_ptr()
+
+
+def _rows_of(x, name: str) -> tuple[int, int]:
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = x.shape[-1]
+    return (x.numel() // cols if cols else 0), cols
+
+
+def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out_dtype=None, out=None, scales=None,
+            residual_out=None):
+    """Root-mean-square norm over the last dimension of a contiguous fp32/bf16
+    CUDA tensor, h / sqrt(mean(h^2) + eps) * weight with h = x + residual
+    (rounded to x's type; h = x without a residual).
+
+    out_dtype: x's type (default), or torch.int8 / torch.float8_e4m3fn for
+    8-bit codes with one fp32 scale per row.  Returns y, or (codes, scales);
+    with a residual, h comes last: (y, h) or (codes, scales, h).  weight: fp32,
+    x.shape[-1] values.  residual_out may be residual or x (updated in place)."""
+    import torch
+    _check_tensor(x, "x")
+    code = _dtype_code(x.dtype)
+    rows, cols = _rows_of(x, "x")
+    dev = x.device
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    q8 = _q8_code(out_dtype)
+    if q8 is None and out_dtype != x.dtype:
+        raise TypeError("out_dtype must be x's dtype, torch.int8 or torch.float8_e4m3fn")
+    if q8 is None and scales is not None:
+        raise ValueError("scales belong to 8-bit outputs")
+    if q8 is not None and cols == 0:
+        raise ValueError("rows without columns have no scale")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    if q8 is not None and scales is None:
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    st = lib().fk_rmsnorm_rows(x.data_ptr(), _like(residual, "residual", x.shape, x.dtype, dev),
+                               _like(weight, "weight", (cols,), torch.float32, dev),
+                               _like(out, "out", x.shape, out_dtype, dev),
+                               _like(scales, "scales", x.shape[:-1], torch.float32, dev),
+                               _like(residual_out, "residual_out", x.shape, x.dtype, dev), rows, cols, code,
+                               code if q8 is None else q8, eps, _stream_handle(x))
+    if st != FK_OK:
+        raise FkError(st, "fk_rmsnorm_rows")
+    if q8 is None:
+        return out if residual is None else (out, residual_out)
+    return (out, scales) if residual is None else (out, scales, residual_out)
+
+
+def rmsnorm_backward(dy, h, weight=None, eps: float = 1e-6, dresidual=None, out=None, dweight=None,
+                     need_dweight: bool = True, workspace=None):
+    """Gradients of rmsnorm (its output in x's type): returns (dx, dweight).
+
+    h: what was normalised (rmsnorm's last result, or its x without a
+    residual); dresidual: gradient that arrives at h from the residual stream,
+    added to dx.  dx is the gradient of x and of residual alike; it may be
+    written over dy, h or dresidual (out=).  dweight is fp32, None when
+    need_dweight is false.  `workspace` (a CUDA tensor of at least
+    fk_rmsnorm_rows_bwd_workspace bytes) makes the call allocation-free."""
+    import torch
+    _check_tensor(h, "h")
+    code = _dtype_code(h.dtype)
+    rows, cols = _rows_of(h, "h")
+    dev = h.device
+    if not need_dweight:
+        if dweight is not None:
+            raise ValueError("dweight given, but need_dweight is false")
+    elif dweight is None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    if out is None:
+        out = torch.empty_like(h)
+    if dy is None:
+        raise TypeError("dy must be a CUDA tensor")
+    args = (_like(dy, "dy", h.shape, h.dtype, dev), h.data_ptr(),
+            _like(weight, "weight", (cols,), torch.float32, dev), _like(dresidual, "dresidual", h.shape, h.dtype, dev),
+            _like(out, "out", h.shape, h.dtype, dev), _like(dweight, "dweight", (cols,), torch.float32, dev), rows,
+            cols, code, eps)
+    if workspace is None:
+        st = lib().fk_rmsnorm_rows_bwd(*args, _stream_handle(h))
+    else:
+        _check_tensor(workspace, "workspace")
+        st = lib().fk_rmsnorm_rows_bwd_ws(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                          _stream_handle(h))
+    if st != FK_OK:
+        raise FkError(st, "fk_rmsnorm_rows_bwd")
+    return out, dweight
+
+
+def quantize_rows(x, dtype=None, gelu: str | None = None, out=None, scales=None):
+    """Rows (the last dimension) of a contiguous fp32/bf16 CUDA tensor to 8-bit
+    codes and one fp32 scale each: (codes, scales), codes * scales[..., None]
+    being the values.  dtype: torch.int8 (default) or torch.float8_e4m3fn;
+    gelu: None, "tanh" or "erf" (or torch's "none", the exact form), applied
+    first."""
+    import torch
+    _check_tensor(x, "x")
+    code = _dtype_code(x.dtype)
+    if gelu not in _EPILOGUES:
+        raise ValueError("gelu must be None, 'tanh' or 'erf'")
+    rows, cols = _rows_of(x, "x")
+    if cols == 0:
+        raise ValueError("rows without columns have no scale")
+    if dtype is None:
+        dtype = torch.int8 if out is None else out.dtype
+    q8 = _q8_code(dtype)
+    if q8 is None:
+        raise TypeError("dtype must be torch.int8 or torch.float8_e4m3fn")
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    if scales is None:
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    st = lib().fk_quantize_rows(x.data_ptr(), _like(out, "out", x.shape, dtype, x.device),
+                                _like(scales, "scales", x.shape[:-1], torch.float32, x.device), rows, cols, code, q8,
+                                _EPILOGUES[gelu], _stream_handle(x))
+    if st != FK_OK:
+        raise FkError(st, "fk_quantize_rows")
+    return out, scales
+
+
+def matmul_q8(a, a_scales, b, b_scales, bias=None, gelu: str | None = None, out_dtype=None, out=None,
+              workspace=None):
+    """act((a @ b.T) * a_scales[..., None] * b_scales + bias) of 8-bit codes:
+    a [..., k] and b [n, k] (a Linear weight), both torch.int8 or both
+    torch.float8_e4m3fn, contiguous CUDA tensors; a_scales [...], b_scales [n]
+    and bias [n] fp32; act: None, "tanh" or "erf" GELU.  Returns [..., n] in
+    out_dtype (bfloat16 by default, or float32).  `workspace` (a CUDA tensor
+    of at least fk_matmul_q8_workspace bytes) makes a call that needs one
+    allocation-free."""
+    import torch
+    _check_tensor(a, "a")
+    _check_tensor(b, "b")
+    q8 = _q8_code(a.dtype)
+    if q8 is None or b.dtype != a.dtype:
+        raise TypeError("a and b must both be torch.int8 or both torch.float8_e4m3fn")
+    if a.dim() == 0 or b.dim() != 2 or b.shape[1] != a.shape[-1] or b.device != a.device:
+        raise ValueError("a is [..., k] and b is [n, k], on one device")
+    if gelu not in _EPILOGUES:
+        raise ValueError("gelu must be None, 'tanh' or 'erf'")
+    n, k = b.shape
+    lead, dev = a.shape[:-1], a.device
+    if a_scales is None or b_scales is None:
+        raise TypeError("a_scales and b_scales must be CUDA tensors")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out is None:
+        out = torch.empty((*lead, n), dtype=out_dtype, device=dev)
+    m = lead.numel()
+    args = (a.data_ptr(), b.data_ptr(), _like(a_scales, "a_scales", lead, torch.float32, dev),
+            _like(b_scales, "b_scales", (n,), torch.float32, dev), _like(bias, "bias", (n,), torch.float32, dev),
+            _like(out, "out", (*lead, n), out_dtype, dev), m, n, k, q8, _dtype_code(out_dtype), _EPILOGUES[gelu])
+    if workspace is None:
+        st = lib().fk_matmul_q8(*args, _stream_handle(a))
+    else:
+        _check_tensor(workspace, "workspace")
+        st = lib().fk_matmul_q8_ws(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _stream_handle(a))
+    if st != FK_OK:
+        raise FkError(st, "fk_matmul_q8")
+    return out
+
+
 __all__ = [
     "FK_OK", "FK_ERR_INVALID_ARG", "FK_ERR_UNSUPPORTED_DTYPE", "FK_ERR_UNSUPPORTED_DEVICE",
     "FK_ERR_CUDA", "FK_F32", "FK_BF16", "FK_GELU_TANH", "FK_GELU_ERF", "FK_PATH_AUTO", "FK_PATH_WARP", "FK_PATH_CTA",
@@ -482,5 +757,8 @@ __all__ = [
     "FK_EPILOGUE_GELU_ERF",
     "fk_status_string", "fk_last_cuda_error", "fk_version", "fk_wait_timeouts",
     "fk_wait_selftest", "make_plan", "gelu_tanh", "gelu",
-    "softmax_rows",
+    "softmax_rows", "FK_I8", "FK_E4M3",
+    "fk_rmsnorm_rows", "fk_rmsnorm_rows_bwd", "fk_rmsnorm_rows_bwd_workspace", "fk_rmsnorm_rows_bwd_ws",
+    "fk_quantize_rows", "fk_matmul_q8", "fk_matmul_q8_workspace", "fk_matmul_q8_ws",
+    "rmsnorm", "rmsnorm_backward", "quantize_rows", "matmul_q8",
 ]

@@ -18,6 +18,7 @@
 
 #include "fk.h"
 #include "fk_internal.h"
+#include "fk_q8_internal.h"
 
 namespace fk {
 namespace {
@@ -176,6 +177,16 @@ fk_status validate_call(const void* x, const void* y, size_t count, size_t esize
   const DeviceInfo* dev = nullptr;
   return check_call(x, y, count, esize, &dev);
 }
+
+fk_status validate_span(const void* p, size_t bytes, size_t align) {
+  if (p == nullptr || reinterpret_cast<uintptr_t>(p) % align != 0) return FK_ERR_INVALID_ARG;
+  int dev = -1;
+  const DeviceInfo* info = current_device_info(&dev);
+  if (info == nullptr || !info->ok || info->major != 10 || info->minor != 0) return FK_ERR_UNSUPPORTED_DEVICE;
+  return check_pointer(p, bytes, dev);
+}
+
+fk_status report_cuda(cudaError_t e) { return e == cudaSuccess ? FK_OK : cuda_fail(e); }
 
 const DeviceInfo* current_device_info(int* device_out) {
   int dev = -1;
@@ -390,11 +401,12 @@ fk_status fk_wait_timeouts(unsigned int* count, int reset) {
   const fk::DeviceInfo* info = fk::current_device_info(&dev);
   if (info == nullptr || !info->ok) return FK_ERR_UNSUPPORTED_DEVICE;
   if (info->major != 10 || info->minor != 0) return FK_ERR_UNSUPPORTED_DEVICE;
-  unsigned a = 0, b = 0, c = 0;
+  unsigned a = 0, b = 0, c = 0, q = 0;
   cudaError_t e = fk::read_wait_timeouts(&a, reset != 0);
   if (e == cudaSuccess) e = fk::read_attention_wait_timeouts(&b, reset != 0);
   if (e == cudaSuccess) e = fk::read_gelu_wait_timeouts(&c, reset != 0);
-  *count = a + b + c;
+  if (e == cudaSuccess) e = fk::read_matmul_wait_timeouts(&q, reset != 0);
+  *count = a + b + c + q;
   return e == cudaSuccess ? FK_OK : fk::cuda_fail(e);
 }
 

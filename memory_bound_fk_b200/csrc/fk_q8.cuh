@@ -1,0 +1,115 @@
+// fk_q8.cuh -- 8-bit codes and per-row scales: the conversions and the row
+// reductions shared by RMSNorm and the row quantiser (sm_100a).
+//
+// A row v becomes scale = max(max |v_j|, 2^-100) / Q and code_j =
+// round(v_j * (Q / max)), nearest even (Q = 127 or 448).  The lower limit on
+// the maximum keeps Q / max finite, so a row of zeros needs no special case.
+// v_j * (Q / max) exceeds Q by at most a rounding, which rounds back to Q.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "fk_common.cuh"
+#include "fk_q8.h"
+
+namespace fk {
+namespace {
+
+constexpr float kTinyAmax = 0x1p-100f;
+
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float absmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+template <int Q8>
+struct Code8;
+
+template <>
+struct Code8<FK_I8> {
+  static constexpr float kMax = 127.0f;
+  // 1.5 * 2^23 + t has unit spacing, so the FMA rounds v * inv itself (the
+  // exact product) to the nearest integer, ties to even, and leaves it in
+  // two's complement in the low mantissa bits.
+  __device__ __forceinline__ static uint32_t one(float v, float inv) {
+    return __float_as_uint(fmaf(v, inv, 12582912.0f));
+  }
+  __device__ __forceinline__ static uint32_t pack4(const float* v, float inv) {
+    const uint32_t lo = __byte_perm(one(v[0], inv), one(v[1], inv), 0x0040);
+    const uint32_t hi = __byte_perm(one(v[2], inv), one(v[3], inv), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+  }
+  __device__ __forceinline__ static uint8_t pack1(float v, float inv) { return static_cast<uint8_t>(one(v, inv)); }
+};
+
+template <>
+struct Code8<FK_E4M3> {
+  static constexpr float kMax = 448.0f;
+  // Two values to two codes (the first in the low byte), nearest even.
+  __device__ __forceinline__ static uint16_t pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  __device__ __forceinline__ static uint32_t pack4(const float* v, float inv) {
+    return pair(v[0] * inv, v[1] * inv) | (static_cast<uint32_t>(pair(v[2] * inv, v[3] * inv)) << 16);
+  }
+  __device__ __forceinline__ static uint8_t pack1(float v, float inv) {
+    return static_cast<uint8_t>(pair(v * inv, 0.0f));
+  }
+};
+
+// What a row's codes are made with: scale is stored, inv multiplies the
+// values; a row that is not finite gets the scale NaN and codes 0 (`ok`).
+struct RowScale {
+  float scale, inv;
+  bool ok;
+};
+template <int Q8>
+__device__ __forceinline__ RowScale row_scale(float amax) {
+  RowScale r;
+  r.ok = amax <= 3.402823466e38f;  // neither NaN nor infinite
+  const float top = fmaxf(amax, kTinyAmax);
+  r.scale = r.ok ? __fdiv_rn(top, Code8<Q8>::kMax) : __int_as_float(0x7fffffff);
+  r.inv = __fdiv_rn(Code8<Q8>::kMax, top);
+  return r;
+}
+
+// Sum of `s` and NaN-propagating maximum of `m` over a warp.
+__device__ __forceinline__ void warp_sum_max(float& s, float& m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    m = absmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+}
+
+// The same over a block of NW warps; `red` holds NW pairs.  The caller puts a
+// __syncthreads() between two uses of `red`.
+template <int NW>
+__device__ __forceinline__ void block_sum_max(float& s, float& m, float2* red) {
+  warp_sum_max(s, m);
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(s, m);
+    __syncthreads();
+    s = red[0].x;
+    m = red[0].y;
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      s += red[w].x;
+      m = absmax_nan(m, red[w].y);
+    }
+  }
+}
+
+// 1 / sqrt(sum / n + eps); NaN for a sum that is not finite, so that a row
+// holding an infinity (or overflowing) is NaN throughout, not zero.
+__device__ __forceinline__ float rms_rstd(float sum, float inv_n, float eps) {
+  return sum <= 3.402823466e38f ? rsqrtf(fmaf(sum, inv_n, eps)) : __int_as_float(0x7fffffff);
+}
+
+}  // namespace
+}  // namespace fk

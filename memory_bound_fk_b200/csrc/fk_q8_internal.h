@@ -1,0 +1,83 @@
+// fk_q8_internal.h -- host-side interfaces between the C ABI of the 8-bit
+// linear layer (fk_q8_api.cu) and its kernel launchers.  Not installed.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "fk_internal.h"
+#include "fk_q8.h"
+
+namespace fk {
+
+// Is [p, p + bytes) memory that the current device may access, wholly inside
+// one allocation?  (p not NULL, aligned to `align`; also checks that the
+// device is a B200.)
+fk_status validate_span(const void* p, size_t bytes, size_t align);
+
+// Keep a CUDA error for fk_last_cuda_error and answer FK_ERR_CUDA (FK_OK for
+// cudaSuccess).
+fk_status report_cuda(cudaError_t e);
+
+// ---- RMSNorm ---------------------------------------------------------------
+// Validated arguments of fk_rmsnorm_rows.  `aligned`: every row of x,
+// residual, h and y (and gamma) allows 16-byte vector access (8- or 4-byte
+// stores for 8-bit y).
+struct RmsnormArgs {
+  const void* x;
+  const void* residual;  // or nullptr
+  const float* gamma;    // or nullptr
+  void* y;
+  float* scales;  // 8-bit outputs only
+  void* h;        // or nullptr
+  size_t rows, cols;
+  int dtype, out_dtype;
+  float eps;
+  bool aligned;
+};
+cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream);
+
+struct RmsnormBwdArgs {
+  const void* dy;
+  const void* h;
+  const float* gamma;
+  const void* dres;
+  void* dx;
+  float* dgamma;
+  size_t rows, cols;
+  int dtype;
+  float eps;
+  bool aligned;
+};
+size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma);
+cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, void* ws, cudaStream_t stream);
+
+// ---- rows to 8 bits ----------------------------------------------------------
+struct QuantizeArgs {
+  const void* x;
+  void* q;
+  float* scales;
+  size_t rows, cols;
+  int dtype, out_dtype, epilogue;
+  bool aligned;
+};
+cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream);
+
+// ---- 8-bit matrix product ----------------------------------------------------
+struct MatmulQ8Args {
+  const void* a;
+  const void* b;
+  const float* a_scales;
+  const float* b_scales;
+  const float* bias;  // or nullptr
+  void* c;
+  size_t m, n, k;
+  int dtype, out_dtype, epilogue;
+};
+// `aligned`: a and b on 16-byte boundaries.
+size_t matmul_q8_workspace(size_t m, size_t n, size_t k, bool aligned);
+cudaError_t launch_matmul_q8(const MatmulQ8Args& a, void* ws, int sm_count, cudaStream_t stream);
+cudaError_t read_matmul_wait_timeouts(unsigned* out, bool reset);
+
+}  // namespace fk
