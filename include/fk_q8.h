@@ -141,8 +141,8 @@ FK_API fk_status fk_quantize_rows(const void *x, void *q, float *scales, size_t 
  *   bias      [in]  n fp32 values, or NULL.
  *   c         [out] m*n values of `out_dtype` (FK_F32 or FK_BF16), row-major
  *             [m, n]; must overlap no input.
- *   m, n, k   m == 0 or n == 0 is a no-op; m, n, k < 2^31; k > 0, and for
- *             FK_I8 k <= 131071 (the exact 32-bit sum of products of codes
+ *   m, n, k   m == 0 or n == 0 is a no-op; m, n, k at most 2^31 - 256; k > 0, and
+ *             for FK_I8 k <= 131071 (the exact 32-bit sum of products of codes
  *             down to -128 cannot overflow).
  *   dtype     FK_I8 (sums exact in 32-bit integers) or FK_E4M3 (sums in fp32
  *             on the tensor cores).

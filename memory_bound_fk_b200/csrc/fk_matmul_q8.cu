@@ -1,98 +1,394 @@
-// fk_matmul_q8.cu -- C = act(A B^T * a_scale * b_scale + bias) with A and B in
-// 8 bits (sm_100a).
+// fk_matmul_q8.cu -- C = act(A B^T * a_scale * b_scale + bias) with A [m, k]
+// and B [n, k] in 8 bits, on the tcgen05 tensor cores (sm_100a).
+//
+// Orientation: the MMA's M side is B (128 output channels), its N side is A
+// (tokens), so that an accumulator's lane is a channel and its column a
+// token.  One token's outputs then lie across the lanes of a warp: they are
+// stored straight from registers as contiguous runs whatever n and the
+// alignment of C, and few tokens make a narrow MMA, not an empty one.
+//
+// Operands come by TMA in boxes of 128 codes of k (one 128-byte swizzled row)
+// and the tensor maps fill what lies outside [m, k] and [n, k] with zeros, so
+// ragged edges need no code in the main loop.
+//
+// The product is bound by reading B once while m is below about 250 (B at
+// 6.5 TB/s against 2 m ops a byte at 3.4 POP/s), by the tensor cores above.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "fk_common.cuh"
-#include "fk_gelu.cuh"
+#include "fk_mm.cuh"
 #include "fk_q8_internal.h"
 
 namespace fk {
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kChan = 128;   // channels per tile (MMA M)
+constexpr int kKBlock = 128; // codes of k per stage (one swizzled row)
+constexpr int kMmThreads = 192;  // four epilogue warps, the load warp, the MMA warp
+constexpr size_t kMaxGrid = 0x7fffffffu;
 
-template <int EPI>
-__device__ __forceinline__ float act(float x) {
-  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f<float>(x);
-  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f<float>(x);
-  return x;
+struct MmParams {
+  const float* sa;
+  const float* sb;
+  const float* bias;
+  void* c;
+  int m, n;
+  int kblocks;  // ceil(k / 128)
+  int tiles_n;  // ceil(n / 128)
+};
+
+// ---------------------------------------------------------------- one tile per block, k split over a cluster
+
+// A block takes 128 channels x TN tokens over a share of k; the SPLIT blocks
+// of a cluster share one tile, push their partial accumulators into the
+// shared memory of the block that owns the tokens, and each finishes TN /
+// SPLIT tokens.  int32 partials add exactly; fp32 ones are added in block
+// order, so results do not depend on timing.
+template <int TN>
+struct SplitShape {
+  static constexpr uint32_t kStageBytes = (kChan + TN) * kKBlock;
+  static constexpr uint32_t kRedBytes = TN * kChan * 4;
+  // about 96 KB of stages, so that two blocks fit an SM: 2 x 96 KB in flight
+  // is more than the 54 KB an SM needs to cover HBM latency at full rate
+  static constexpr int kStages = TN >= 128 ? 3 : TN >= 64 ? 4 : 5;
+  static constexpr uint32_t kTmemCols = TN < 32 ? 32 : TN;
+};
+
+template <int Q8, int TN, int SPLIT, typename T, int EPI>
+__global__ void __launch_bounds__(kMmThreads)
+    matmul_split_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
+                        MmParams p) {
+  using S = SplitShape<TN>;
+  constexpr int ST = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[ST], empty[ST], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ uint32_t part_bad[SPLIT];  // whether a block of the cluster gave up on a wait
+  __shared__ float s_sa[TN];
+  // stages of [128 channels | TN tokens] x 128 codes, 1024-byte aligned
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  uint32_t* red = reinterpret_cast<uint32_t*>(base + ST * S::kStageBytes);  // [SPLIT][TN / SPLIT][128]
+
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int part = SPLIT > 1 ? static_cast<int>(blockIdx.x % SPLIT) : 0;
+  const unsigned tile = blockIdx.x / SPLIT;
+  const int n0 = static_cast<int>(tile % p.tiles_n) * kChan, m0 = static_cast<int>(tile / p.tiles_n) * TN;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.kblocks) * part / SPLIT);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (part + 1) / SPLIT);
+  volatile int* abort = &abort_flag;
+
+  if (warp == 5) tc::tmem_alloc(&tmem_slot, S::kTmemCols);
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (tid < TN) s_sa[tid] = m0 + tid < p.m ? p.sa[m0 + tid] : 0.0f;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if constexpr (SPLIT > 1) cluster_arrive_relaxed();  // every block of the cluster has started: waited for below
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 4) {
+    if ((tid & 31) == 0) {
+      int i = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int st = i % ST;
+        if (i >= ST && !mm::wait(&empty[st], (i / ST - 1) & 1, abort)) break;
+        uint8_t* dst = base + st * S::kStageBytes;
+        mbar_arrive_expect_tx(&full[st], S::kStageBytes);
+        tc::tma_load_2d(dst, &tma_b, &full[st], kb * kKBlock, n0);
+        tc::tma_load_2d(dst + kChan * kKBlock, &tma_a, &full[st], kb * kKBlock, m0);
+      }
+      // copies in flight land before the block exits (all have, unless a wait gave up)
+      for (int j = i > ST ? i - ST : 0; j < i; ++j) mm::drain(&full[j % ST], (j / ST) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if ((tid & 31) == 0) {
+      constexpr uint32_t HI = tc::smem_desc_hi(1024);
+      constexpr uint32_t ID = mm::idesc<Q8>(kChan, TN);
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int st = i % ST;
+        if (!mm::wait(&full[st], (i / ST) & 1, abort)) break;
+        tc::fence_after_sync();
+        const uint32_t a = tc::smem_desc_lo(smem_addr(base + st * S::kStageBytes), 16);
+        const uint32_t b = a + kChan * kKBlock / 16;
+#pragma unroll
+        for (int q = 0; q < kKBlock / 32; ++q)
+          mm::mma<Q8>(tmem, tc::desc_join(a + 2 * q, HI), tc::desc_join(b + 2 * q, HI), ID, (i | q) != 0);
+        tc::mma_commit(&empty[st]);
+      }
+      tc::mma_commit(&done);
+    }
+    __syncwarp();
+  }
+  if constexpr (SPLIT > 1) cluster_wait();
+
+  // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, lane = channel
+  if (warp < 4) {
+    mm::drain(&done, 0);
+    tc::fence_after_sync();
+  }
+  const int chan = n0 + tid;
+  const bool good = *abort == 0;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+  float sb = 0.0f, bias = 0.0f;
+  if (warp < 4 && chan < p.n) {
+    sb = p.sb[chan];
+    bias = p.bias ? p.bias[chan] : 0.0f;
+  }
+  T* c = static_cast<T*>(p.c);
+  auto finish = [&](uint32_t w, int t) {
+    const float v = mm::act<EPI>(mm::acc_value<Q8>(w) * s_sa[t] * sb + bias);
+    if (chan < p.n && m0 + t < p.m) c[static_cast<size_t>(m0 + t) * p.n + chan] = static_cast<T>(v);
+  };
+  if constexpr (SPLIT == 1) {
+    if (warp < 4 && good) {
+#pragma unroll 1
+      for (int t = 0; t < TN && m0 + t < p.m; t += 16) {
+        uint32_t r[16];
+        mm::tmem_ld16(lane_base + t, r);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) finish(r[q], t + q);
+      }
+    }
+  } else {
+    constexpr int OWN = TN / SPLIT;  // tokens this block finishes
+    if (warp < 4) {
+#pragma unroll 1
+      for (int t = 0; t < TN && m0 + t < p.m; t += 16) {
+        uint32_t r[16];
+        mm::tmem_ld16(lane_base + t, r);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int owner = (t + q) / OWN, slot = (t + q) % OWN;
+          mm::st_cluster(cluster_addr(red + (part * OWN + slot) * kChan + tid, owner), r[q]);
+        }
+      }
+    }
+    if (tid < SPLIT) mm::st_cluster(cluster_addr(&part_bad[part], tid), good ? 0u : 1u);
+    mm::cluster_sync();
+    bool all_good = true;
+#pragma unroll
+    for (int o = 0; o < SPLIT; ++o) all_good = all_good && part_bad[o] == 0;
+    if (warp < 4 && all_good) {
+#pragma unroll
+      for (int s = 0; s < OWN; ++s) {
+        const int t = part * OWN + s;
+        if (m0 + t >= p.m) break;
+        uint32_t w = red[s * kChan + tid];
+#pragma unroll
+        for (int o = 1; o < SPLIT; ++o) w = mm::acc_add<Q8>(w, red[(o * OWN + s) * kChan + tid]);
+        finish(w, t);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) tc::tmem_dealloc(tmem, S::kTmemCols);
 }
 
-template <int Q8>
-struct Acc;
-template <>
-struct Acc<FK_I8> {
-  using type = int;
-  __device__ static int load(uint8_t c) { return static_cast<int8_t>(c); }
-};
-template <>
-struct Acc<FK_E4M3> {
-  using type = float;
-  __device__ static float load(uint8_t c) { return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3))); }
+// ---------------------------------------------------------------- rows padded to 16 bytes
+
+// dst [rows, kp] <- src [rows, k] (any alignment), zeros past k; kp is k
+// rounded up to 16.  One thread per 16 bytes of dst: five aligned words and a
+// funnel shift, or single bytes next to the ends of src.
+__global__ void __launch_bounds__(256)
+    matmul_pad_kernel(const uint8_t* src, uint4* dst, size_t rows, size_t k, size_t chunks) {
+  const size_t total = rows * chunks, end = rows * k;
+  for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<size_t>(gridDim.x) * 256) {
+    const size_t row = i / chunks, l = (i - row * chunks) * 16, at = row * k + l;
+    uint32_t w[4];
+    const size_t shift = (reinterpret_cast<uintptr_t>(src) + at) & 3;
+    if (at >= shift && at - shift + 20 <= end) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(src + at - shift);
+      uint32_t v[5];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) v[j] = __ldg(q + j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], static_cast<unsigned>(shift) * 8);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (at + 4 * j + b < end) w[j] |= static_cast<uint32_t>(src[at + 4 * j + b]) << (8 * b);
+      }
+    }
+    const size_t left = k - l;  // codes of this row from here on
+    if (left < 16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int keep = static_cast<int>(left) - 4 * j;
+        w[j] = keep <= 0 ? 0u : keep >= 4 ? w[j] : w[j] & ((1u << (8 * keep)) - 1u);
+      }
+    }
+    dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+using PFN_encodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+PFN_encodeTiled encode_fn() {
+  static PFN_encodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return static_cast<PFN_encodeTiled>(nullptr);
+    }
+    return reinterpret_cast<PFN_encodeTiled>(p);
+  }();
+  return fn;
+}
+
+// [rows, k] codes with a row pitch of `pitch` bytes (a multiple of 16), in
+// boxes of 128 codes x box_rows rows, 128-byte swizzle; outside reads 0.
+bool make_map(CUtensorMap* m, const void* ptr, size_t rows, size_t k, size_t pitch, int box_rows) {
+  PFN_encodeTiled f = encode_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  const cuuint32_t box[2] = {kKBlock, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A product whose operands TMA can read.
+struct MmCall {
+  const void *a, *b;
+  size_t k, pitch;
+  MatmulQ8Args p;
+  int sm_count;
+  cudaStream_t stream;
 };
 
-// One thread per output, 16 x 16 outputs per block, k in steps of 16 through
-// shared memory.
-template <int Q8, typename T, int EPI>
-__global__ void __launch_bounds__(kTile* kTile) matmul_simple_kernel(MatmulQ8Args p) {
-  using A = typename Acc<Q8>::type;
-  __shared__ A sa[kTile][kTile + 1], sb[kTile][kTile + 1];
-  const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-  const size_t tiles_n = (p.n + kTile - 1) / kTile, tiles = tiles_n * ((p.m + kTile - 1) / kTile);
-  for (size_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const size_t i0 = t / tiles_n * kTile, j0 = t % tiles_n * kTile;
-    A acc = 0;
-    for (size_t l0 = 0; l0 < p.k; l0 += kTile) {
-      const size_t l = l0 + tx, i = i0 + ty, j = j0 + ty;
-      sa[ty][tx] = i < p.m && l < p.k ? Acc<Q8>::load(static_cast<const uint8_t*>(p.a)[i * p.k + l]) : A(0);
-      sb[ty][tx] = j < p.n && l < p.k ? Acc<Q8>::load(static_cast<const uint8_t*>(p.b)[j * p.k + l]) : A(0);
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kTile; ++q) acc += sa[ty][q] * sb[tx][q];
-      __syncthreads();
-    }
-    const size_t i = i0 + ty, j = j0 + tx;
-    if (i < p.m && j < p.n) {
-      float v = static_cast<float>(acc) * p.a_scales[i] * p.b_scales[j];
-      if (p.bias) v += p.bias[j];
-      static_cast<T*>(p.c)[i * p.n + j] = static_cast<T>(act<EPI>(v));
-    }
+template <int Q8, int TN, int SPLIT, typename T, int EPI>
+cudaError_t launch_split(const MmCall& c) {
+  using S = SplitShape<TN>;
+  const size_t tiles_n = (c.p.n + kChan - 1) / kChan, tiles_m = (c.p.m + TN - 1) / TN;
+  if (tiles_m > kMaxGrid / SPLIT / tiles_n) return cudaErrorInvalidConfiguration;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, c.a, c.p.m, c.k, c.pitch, TN) || !make_map(&mb, c.b, c.p.n, c.k, c.pitch, kChan))
+    return cudaErrorInvalidValue;
+  const size_t smem = S::kStages * S::kStageBytes + (SPLIT > 1 ? S::kRedBytes : 0) + 1024;
+  auto kernel = matmul_split_kernel<Q8, TN, SPLIT, T, EPI>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  MmParams p = {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m), static_cast<int>(c.p.n),
+                static_cast<int>((c.k + kKBlock - 1) / kKBlock), static_cast<int>(tiles_n)};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles_n * tiles_m * SPLIT));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = SPLIT;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = SPLIT > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+}
+
+// Blocks of a cluster that share a tile: doubled while the grid still fits
+// two blocks per SM at once and each keeps at least four 128-code steps of k.
+template <int Q8, int TN, typename T, int EPI>
+cudaError_t launch_tokens(const MmCall& c) {
+  const size_t tiles = ((c.p.n + kChan - 1) / kChan) * ((c.p.m + TN - 1) / TN);
+  const size_t kblocks = (c.k + kKBlock - 1) / kKBlock, room = 2 * static_cast<size_t>(c.sm_count);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= room && kblocks >= static_cast<size_t>(split) * 2 * 4) split *= 2;
+  switch (split) {
+    case 1: return launch_split<Q8, TN, 1, T, EPI>(c);
+    case 2: return launch_split<Q8, TN, 2, T, EPI>(c);
+    case 4: return launch_split<Q8, TN, 4, T, EPI>(c);
+    default: return launch_split<Q8, TN, 8, T, EPI>(c);
   }
 }
 
 template <int Q8, typename T, int EPI>
-cudaError_t launch_epi(const MatmulQ8Args& p, cudaStream_t s) {
-  const size_t tiles = ((p.n + kTile - 1) / kTile) * ((p.m + kTile - 1) / kTile);
-  matmul_simple_kernel<Q8, T, EPI><<<static_cast<unsigned>(tiles < 0x7fffffffu ? tiles : 0x7fffffffu), kTile * kTile, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_epi(const MmCall& c) {
+  if (c.p.m <= 16) return launch_tokens<Q8, 16, T, EPI>(c);
+  if (c.p.m <= 32) return launch_tokens<Q8, 32, T, EPI>(c);
+  if (c.p.m <= 64) return launch_tokens<Q8, 64, T, EPI>(c);
+  return launch_tokens<Q8, 128, T, EPI>(c);
 }
 
 template <int Q8, typename T>
-cudaError_t launch_out(const MatmulQ8Args& p, cudaStream_t s) {
-  switch (p.epilogue) {
-    case FK_EPILOGUE_GELU_TANH: return launch_epi<Q8, T, FK_EPILOGUE_GELU_TANH>(p, s);
-    case FK_EPILOGUE_GELU_ERF: return launch_epi<Q8, T, FK_EPILOGUE_GELU_ERF>(p, s);
-    default: return launch_epi<Q8, T, FK_EPILOGUE_NONE>(p, s);
+cudaError_t launch_out(const MmCall& c) {
+  switch (c.p.epilogue) {
+    case FK_EPILOGUE_GELU_TANH: return launch_epi<Q8, T, FK_EPILOGUE_GELU_TANH>(c);
+    case FK_EPILOGUE_GELU_ERF: return launch_epi<Q8, T, FK_EPILOGUE_GELU_ERF>(c);
+    default: return launch_epi<Q8, T, FK_EPILOGUE_NONE>(c);
   }
 }
 
 template <int Q8>
-cudaError_t launch_type(const MatmulQ8Args& p, cudaStream_t s) {
-  return p.out_dtype == FK_F32 ? launch_out<Q8, float>(p, s) : launch_out<Q8, __nv_bfloat16>(p, s);
+cudaError_t launch_type(const MmCall& c) {
+  return c.p.out_dtype == FK_F32 ? launch_out<Q8, float>(c) : launch_out<Q8, __nv_bfloat16>(c);
+}
+
+size_t round16(size_t v) { return (v + 15) / 16 * 16; }
+
+cudaError_t launch_pad(const void* src, void* dst, size_t rows, size_t k, cudaStream_t s) {
+  const size_t chunks = round16(k) / 16, blocks = (rows * chunks + 255) / 256;
+  matmul_pad_kernel<<<static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, s>>>(
+      static_cast<const uint8_t*>(src), static_cast<uint4*>(dst), rows, k, chunks);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t matmul_q8_workspace(size_t, size_t, size_t, bool) { return 0; }
-
-cudaError_t launch_matmul_q8(const MatmulQ8Args& p, void*, int, cudaStream_t s) {
-  return p.dtype == FK_I8 ? launch_type<FK_I8>(p, s) : launch_type<FK_E4M3>(p, s);
+size_t matmul_q8_workspace(size_t m, size_t n, size_t k, bool aligned) {
+  return aligned && k % 16 == 0 ? 0 : (m + n) * round16(k);
 }
 
-cudaError_t read_matmul_wait_timeouts(unsigned* out, bool) {
-  *out = 0;
-  return cudaSuccess;
+cudaError_t launch_matmul_q8(const MatmulQ8Args& p, void* ws, int sm_count, cudaStream_t s) {
+  MmCall c = {p.a, p.b, p.k, p.k, p, sm_count > 0 ? sm_count : 1, s};
+  if (ws != nullptr) {
+    // operands that TMA cannot read as they are
+    const size_t kp = round16(p.k);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    if (p.k % 16 != 0 || reinterpret_cast<uintptr_t>(p.a) % 16 != 0) {
+      const cudaError_t e = launch_pad(p.a, w, p.m, p.k, s);
+      if (e != cudaSuccess) return e;
+      c.a = w;
+    }
+    if (p.k % 16 != 0 || reinterpret_cast<uintptr_t>(p.b) % 16 != 0) {
+      const cudaError_t e = launch_pad(p.b, w + p.m * kp, p.n, p.k, s);
+      if (e != cudaSuccess) return e;
+      c.b = w + p.m * kp;
+    }
+    c.k = c.pitch = kp;
+  }
+  return p.dtype == FK_I8 ? launch_type<FK_I8>(c) : launch_type<FK_E4M3>(c);
+}
+
+cudaError_t read_matmul_wait_timeouts(unsigned* out, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, mm::g_mm_wait_timeouts, sizeof(unsigned));
+  if (e == cudaSuccess && reset) {
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(mm::g_mm_wait_timeouts, &zero, sizeof(unsigned));
+  }
+  return e;
 }
 
 }  // namespace fk

@@ -1,0 +1,117 @@
+// fk_mm.cuh -- sm_100a plumbing of the 8-bit matrix product that fk_tc.cuh
+// does not hold: instruction descriptors and issue of the 8-bit MMAs, raw
+// 32-bit TMEM loads, cluster helpers, and the kernel's bounded waits.
+#pragma once
+
+#include <stdint.h>
+
+#include "fk_gelu.cuh"
+#include "fk_q8.h"
+#include "fk_sync.cuh"
+#include "fk_tc.cuh"
+
+namespace fk {
+namespace mm {
+
+// Threads of the product's kernels whose bounded wait gave up.
+__device__ unsigned g_mm_wait_timeouts;
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+// Bounded mbarrier wait: gives up after 1 s, is counted, and raises the
+// block's abort flag, on which its other waits return at once.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;  // suspended up to 20 us per try
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitNs) {
+      atomicAdd(&g_mm_wait_timeouts, 1u);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+// Bounded wait that ignores the abort flag: copies and MMAs in flight land
+// before the block goes on to exit.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (global_ns() - t0 > kWaitNs) {
+      atomicAdd(&g_mm_wait_timeouts, 1u);
+      return;
+    }
+  }
+}
+
+// Instruction descriptor of a dense 8-bit MMA, both operands K-major, M x N:
+// kind::i8 (signed codes, 32-bit integer accumulator) or kind::f8f6f4 (e4m3,
+// fp32 accumulator).  One instruction covers 32 codes of k for either.
+template <int Q8>
+__host__ __device__ constexpr uint32_t idesc(int m, int n) {
+  constexpr uint32_t fmt = Q8 == FK_I8 ? 1u : 0u;  // A and B: signed integer / e4m3
+  constexpr uint32_t acc = Q8 == FK_I8 ? 2u : 1u;  // accumulator: s32 / f32
+  return (acc << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D (M x N, tensor memory) = A B^T (+ D when accumulate != 0), operands in
+// shared memory.  Issued by one thread.
+template <int Q8>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (Q8 == FK_I8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 consecutive 32-bit TMEM columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// All threads of the cluster: arrive with release, wait with acquire.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Accumulator word to fp32: the exact integer sum rounded once, or the sum.
+template <int Q8>
+__device__ __forceinline__ float acc_value(uint32_t w) {
+  return Q8 == FK_I8 ? static_cast<float>(static_cast<int>(w)) : __uint_as_float(w);
+}
+template <int Q8>
+__device__ __forceinline__ uint32_t acc_add(uint32_t a, uint32_t b) {
+  return Q8 == FK_I8 ? a + b : __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+
+template <int EPI>
+__device__ __forceinline__ float act(float x) {
+  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f<float>(x);
+  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f<float>(x);
+  return x;
+}
+
+}  // namespace mm
+}  // namespace fk

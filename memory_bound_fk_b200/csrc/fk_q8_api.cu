@@ -126,7 +126,7 @@ fk_status matmul_call(const void* a, const void* b, const float* a_scales, const
   if (!q8_dtype(dtype) || !float_dtype(out_dtype)) return FK_ERR_UNSUPPORTED_DTYPE;
   if (!known_epilogue(epilogue)) return FK_ERR_INVALID_ARG;
   if (m == 0 || n == 0) return FK_OK;
-  constexpr size_t kLimit = (size_t{1} << 31) - 1;
+  constexpr size_t kLimit = (size_t{1} << 31) - 256;  // tile indexes stay in 32 bits
   if (k == 0 || m > kLimit || n > kLimit || k > kLimit || (dtype == FK_I8 && k > 131071)) return FK_ERR_INVALID_ARG;
   if (a == nullptr || b == nullptr || a_scales == nullptr || b_scales == nullptr || c == nullptr)
     return FK_ERR_INVALID_ARG;
@@ -241,7 +241,7 @@ fk_status fk_matmul_q8_ws(const void* a, const void* b, const float* a_scales, c
 
 fk_status fk_matmul_q8_workspace(size_t m, size_t n, size_t k, int aligned, size_t* bytes) {
   if (bytes == nullptr) return FK_ERR_INVALID_ARG;
-  constexpr size_t kLimit = (size_t{1} << 31) - 1;
+  constexpr size_t kLimit = (size_t{1} << 31) - 256;  // tile indexes stay in 32 bits
   *bytes = 0;
   if (m == 0 || n == 0) return FK_OK;
   if (k == 0 || m > kLimit || n > kLimit || k > kLimit) return FK_ERR_INVALID_ARG;
