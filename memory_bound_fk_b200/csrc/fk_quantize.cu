@@ -6,6 +6,7 @@
 #include "fk_gelu.cuh"
 #include "fk_q8.cuh"
 #include "fk_q8_internal.h"
+#include "fk_q8_rows.cuh"
 
 namespace fk {
 namespace {
@@ -18,6 +19,45 @@ __device__ __forceinline__ float act(float x) {
   if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f<float>(x);
   if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f<float>(x);
   return x;
+}
+
+// ---------------------------------------------------------------- rows held in registers
+
+// Two values at a time (packed fp32 arithmetic).
+template <int EPI>
+__device__ __forceinline__ float2 act2(float2 x) {
+  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f2<float>(x);
+  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f2<float>(x);
+  return x;
+}
+
+template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, bool WARP, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(QuantizeArgs a) {
+  constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
+  __shared__ float2 red[WARP ? 1 : MAXT / 32];
+  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, const Place& p) {
+    const size_t base = row * a.cols;
+    uint4 raw[VPT];
+    load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.x) + base, p, raw);
+    float v[EPT], s = 0.0f, m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      Elem<T>::unpack(raw[c], v + c * VEC);
+#pragma unroll
+      for (int k = 0; k < VEC; k += 2) {
+        const float2 z = act2<EPI>(make_float2(v[c * VEC + k], v[c * VEC + k + 1]));
+        v[c * VEC + k] = z.x;
+        v[c * VEC + k + 1] = z.y;
+        m = absmax_nan(absmax_nan(m, z.x), z.y);
+      }
+    }
+    team_sum_max<WARP>(s, m, red);
+    const RowScale q = row_scale<OUT>(m);
+    if (p.t == 0) a.scales[row] = q.scale;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c)
+      store_codes<T, OUT, ALIGNED>(static_cast<uint8_t*>(a.q) + base, p, c, v + c * VEC, q);
+  });
 }
 
 // ---------------------------------------------------------------- streaming path
@@ -42,10 +82,38 @@ __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(Quantiz
   }
 }
 
+template <typename T, int OUT, int EPI, bool ALIGNED>
+void launch_rows(const QuantizeArgs& a, cudaStream_t s) {
+  if (a.cols <= kRowWarpCols) {
+    const RowLaunch l = warp_launch(a.rows);
+    if (a.cols <= kRowWarpCols / 4)
+      quantize_row_kernel<T, OUT, EPI, 8, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+    else if (a.cols <= kRowWarpCols / 2)
+      quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+    else
+      quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+  } else if (a.cols <= kRowSmallCols) {
+    const RowLaunch l = block_launch(a.rows, a.cols, 16);
+    quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+  } else if (a.cols <= kRowLargeCols) {
+    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+    quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+  } else {
+    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+    quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 1024, 1><<<l.grid, l.threads, 0, s>>>(a);
+  }
+}
+
 template <typename T, int OUT, int EPI>
 cudaError_t launch_epi(const QuantizeArgs& a, cudaStream_t s) {
-  const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
-  quantize_stream_kernel<T, OUT, EPI><<<g, kStreamThreads, 0, s>>>(a);
+  if (a.cols > kRowMaxCols) {
+    const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
+    quantize_stream_kernel<T, OUT, EPI><<<g, kStreamThreads, 0, s>>>(a);
+  } else if (a.aligned) {
+    launch_rows<T, OUT, EPI, true>(a, s);
+  } else {
+    launch_rows<T, OUT, EPI, false>(a, s);
+  }
   return cudaGetLastError();
 }
 

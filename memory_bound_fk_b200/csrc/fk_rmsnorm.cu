@@ -10,6 +10,7 @@
 #include "fk_common.cuh"
 #include "fk_q8.cuh"
 #include "fk_q8_internal.h"
+#include "fk_q8_rows.cuh"
 
 namespace fk {
 namespace {
@@ -22,6 +23,68 @@ template <typename T>
 __device__ __forceinline__ float round_to(float v) {
   if constexpr (sizeof(T) == 4) return v;
   return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+// ---------------------------------------------------------------- rows held in registers
+
+// MAXT, MINB: threads and blocks per SM the registers are sized for (64 a
+// thread for 1024 threads on an SM).
+template <typename T, int OUT, int EPT, bool ALIGNED, bool WARP, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(RmsnormArgs a) {
+  constexpr bool Q8 = OUT == FK_I8 || OUT == FK_E4M3;
+  constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
+  __shared__ float2 red[WARP ? 1 : MAXT / 32];
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, const Place& p) {
+    const size_t base = row * a.cols;
+    uint4 raw[VPT];
+    load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.x) + base, p, raw);
+    if (a.residual) {
+      uint4 res[VPT];
+      load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.residual) + base, p, res);
+#pragma unroll
+      for (int c = 0; c < VPT; ++c) {
+        float f[VEC], r[VEC];
+        Elem<T>::unpack(raw[c], f);
+        Elem<T>::unpack(res[c], r);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] += r[k];
+        raw[c] = Elem<T>::pack(f);  // h, rounded to the rows' type: what is normalised is what is stored
+        if (a.h) store_place<T, ALIGNED>(static_cast<T*>(a.h) + base, p, c, raw[c]);
+      }
+    }
+    float v[EPT], s = 0.0f, m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float g[VEC];
+      Elem<T>::unpack(raw[c], v + c * VEC);
+      load_params<VEC, ALIGNED>(a.gamma, p, c, g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        float& f = v[c * VEC + k];
+        s = fmaf(f, f, s);
+        f *= g[k];
+        if (Q8) m = absmax_nan(m, f);
+      }
+    }
+    team_sum_max<WARP>(s, m, red);
+    const float rstd = rms_rstd(s, inv_n, a.eps);
+    RowScale q;
+    if constexpr (Q8) {
+      q = row_scale<OUT>(m * rstd);
+      if (p.t == 0) a.scales[row] = q.scale;
+    }
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float o[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) o[k] = v[c * VEC + k] * rstd;
+      if constexpr (Q8)
+        store_codes<T, OUT, ALIGNED>(static_cast<uint8_t*>(a.y) + base, p, c, o, q);
+      else
+        store_place<T, ALIGNED>(static_cast<T*>(a.y) + base, p, c, Elem<T>::pack(o));
+    }
+  });
 }
 
 // ---------------------------------------------------------------- streaming path
@@ -74,10 +137,38 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
   }
 }
 
+template <typename T, int OUT, bool ALIGNED>
+void launch_rows(const RmsnormArgs& a, cudaStream_t s) {
+  if (a.cols <= kRowWarpCols) {
+    const RowLaunch l = warp_launch(a.rows);
+    if (a.cols <= kRowWarpCols / 4)
+      rmsnorm_row_kernel<T, OUT, 8, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+    else if (a.cols <= kRowWarpCols / 2)
+      rmsnorm_row_kernel<T, OUT, 16, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+    else
+      rmsnorm_row_kernel<T, OUT, 32, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+  } else if (a.cols <= kRowSmallCols) {
+    const RowLaunch l = block_launch(a.rows, a.cols, 16);
+    rmsnorm_row_kernel<T, OUT, 16, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+  } else if (a.cols <= kRowLargeCols) {
+    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+    rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+  } else {
+    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+    rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 1024, 1><<<l.grid, l.threads, 0, s>>>(a);
+  }
+}
+
 template <typename T, int OUT>
 cudaError_t launch_out(const RmsnormArgs& a, cudaStream_t s) {
-  const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
-  rmsnorm_stream_kernel<T, OUT><<<g, kStreamThreads, 0, s>>>(a);
+  if (a.cols > kRowMaxCols) {
+    const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
+    rmsnorm_stream_kernel<T, OUT><<<g, kStreamThreads, 0, s>>>(a);
+  } else if (a.aligned) {
+    launch_rows<T, OUT, true>(a, s);
+  } else {
+    launch_rows<T, OUT, false>(a, s);
+  }
   return cudaGetLastError();
 }
 
