@@ -95,7 +95,7 @@ FK_API fk_status fk_rmsnorm_rows(const void *x, const void *residual, const floa
  *   dgamma [out] cols fp32 values, or NULL (not computed).  rows == 0 gives 0.
  *   eps    as in the forward call.
  * Arithmetic in fp32; dgamma is summed in fp32 in an order fixed by the
- * shape (two equal calls give equal bits).  Rows up to 16384 columns are
+ * shape (two equal calls give equal bits).  Rows up to 32768 columns are
  * read once.
  * Errors as fk_rmsnorm_rows; dgamma must overlap nothing.
  */

@@ -105,6 +105,16 @@ __device__ __forceinline__ void block_sum_max(float& s, float& m, float2* red) {
   }
 }
 
+// A pair of values into a block's shared memory at cluster address `dst`.
+__device__ __forceinline__ void st_cluster_f2(uint32_t dst, float a, float b) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(a), "f"(b) : "memory");
+}
+
+// Every thread of the cluster: what was stored before it is seen after it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // 1 / sqrt(sum / n + eps); NaN for a sum that is not finite, so that a row
 // holding an infinity (or overflowing) is NaN throughout, not zero.
 __device__ __forceinline__ float rms_rstd(float sum, float inv_n, float eps) {

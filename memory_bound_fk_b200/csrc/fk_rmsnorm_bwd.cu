@@ -10,6 +10,8 @@
 #include "fk_common.cuh"
 #include "fk_q8.cuh"
 #include "fk_q8_internal.h"
+#include "fk_q8_rows.cuh"
+#include "fk_sync.cuh"
 
 namespace fk {
 namespace {
@@ -17,7 +19,159 @@ namespace {
 constexpr int kStreamThreads = 512;
 constexpr size_t kMaxGrid = 0x7fffffffu;
 constexpr int kColThreads = 128;      // columns per block of the column sums
+constexpr int kJoinCols = 32, kJoinWays = 16;
+constexpr int kBwdEpt = 16;           // values a thread holds of a row (8 or 32 in a warp team where that fits better)
+constexpr int kBwdThreads = 512;
+constexpr size_t kBwdBlockCols = kBwdEpt * kBwdThreads;  // columns a block holds
+constexpr int kSmCount = 148;
 constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
+
+// ---------------------------------------------------------------- rows held in registers
+
+// Blocks that stay on the GPU and walk the rows.  The team of a row is a warp
+// (CL = 0: up to 1024 columns), a block (CL = 1: up to 8192), or a cluster of
+// CL blocks, so that a thread's columns never change: gamma and the running
+// dgamma sums live in its registers.  The next row's h and dy are loaded
+// before the current one is reduced (PF), which keeps HBM busy through the
+// reduction.  At the end each block writes its columns' partial sums, one row
+// of workspace per team block (the warps of a warp-team block added first, in
+// order).
+//
+// Bound by HBM.  16 values a thread and as many registers as they take (two
+// 256-thread blocks per SM).  Measured on B200 (64M bf16 values, four streams
+// of them, event overhead taken off): 4096 columns 5.99 TB/s; without the
+// prefetch 4.79; with registers capped for three blocks per SM 4.18 (spills);
+// 8 values a thread 5.61.  8192 columns (one 512-thread block per SM) 5.86.
+// 16384 columns in one block: 3.4 TB/s at 32 values a thread, 3.0 with 1024
+// threads, hence the clusters.
+template <typename T, int EPT, bool ALIGNED, int CL, bool PF, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs a, float* partial) {
+  constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
+  constexpr bool WARP = CL == 0;
+  constexpr int TEAMS = CL > 1 ? CL : 1;
+  // two scratch rows in turn, one pair per warp of the team: one barrier a row
+  __shared__ float2 red[2][WARP ? 1 : TEAMS * (MAXT / 32)];
+  const int cols = static_cast<int>(a.cols);
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const Place p = WARP ? Place{static_cast<int>(threadIdx.x & 31), 32, cols}
+                       : Place{static_cast<int>(rank * blockDim.x + threadIdx.x), static_cast<int>(TEAMS * blockDim.x), cols};
+  const size_t team = WARP ? static_cast<size_t>(blockIdx.x) * warps + warp : blockIdx.x / TEAMS;
+  const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps : gridDim.x / TEAMS;
+  const T* const h = static_cast<const T*>(a.h);
+  const T* const dy = static_cast<const T*>(a.dy);
+  if constexpr (CL > 1) cluster_arrive_relaxed();  // every block has started: waited for before the first push
+  float gam[EPT], acc[EPT];
+#pragma unroll
+  for (int c = 0; c < VPT; ++c) load_params<VEC, ALIGNED>(a.gamma, p, c, gam + c * VEC);
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
+  uint4 rh[VPT], rd[VPT];
+  if (PF && team < a.rows) {
+    load_place<T, VPT, ALIGNED>(h + team * a.cols, p, rh);
+    load_place<T, VPT, ALIGNED>(dy + team * a.cols, p, rd);
+  }
+  if constexpr (CL > 1) cluster_wait();
+  int turn = 0;
+  for (size_t row = team; row < a.rows; row += stride) {
+    const size_t base = row * a.cols;
+    uint4 nh[VPT], nd[VPT], rr[VPT];
+    if (!PF) {
+      load_place<T, VPT, ALIGNED>(h + base, p, rh);
+      load_place<T, VPT, ALIGNED>(dy + base, p, rd);
+    }
+    if (a.dres) load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.dres) + base, p, rr);
+    if (PF && row + stride < a.rows) {
+      load_place<T, VPT, ALIGNED>(h + base + stride * a.cols, p, nh);
+      load_place<T, VPT, ALIGNED>(dy + base + stride * a.cols, p, nd);
+    }
+    float s = 0.0f, d = 0.0f;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float f[VEC], g[VEC];
+      Elem<T>::unpack(rh[c], f);
+      Elem<T>::unpack(rd[c], g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        s = fmaf(f[k], f[k], s);
+        d = fmaf(g[k] * gam[c * VEC + k], f[k], d);
+      }
+    }
+    s = warp_sum(s);
+    d = warp_sum(d);
+    if constexpr (!WARP) {
+      if constexpr (CL > 1) {
+        if ((threadIdx.x & 31) < TEAMS)
+          st_cluster_f2(cluster_addr(&red[turn][rank * warps + warp], threadIdx.x & 31), s, d);
+        cluster_barrier();
+      } else {
+        if ((threadIdx.x & 31) == 0) red[turn][warp] = make_float2(s, d);
+        __syncthreads();
+      }
+      s = red[turn][0].x;
+      d = red[turn][0].y;
+      for (int w = 1; w < TEAMS * warps; ++w) {
+        s += red[turn][w].x;
+        d += red[turn][w].y;
+      }
+      turn ^= 1;
+    }
+    const float r = rms_rstd(s, inv_n, a.eps);
+    const float r3s = r * r * r * (d * inv_n);
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float f[VEC], g[VEC], o[VEC];
+      Elem<T>::unpack(rh[c], f);
+      Elem<T>::unpack(rd[c], g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        acc[c * VEC + k] = fmaf(g[k] * f[k], r, acc[c * VEC + k]);
+        o[k] = fmaf(r, g[k] * gam[c * VEC + k], -r3s * f[k]);
+      }
+      if (a.dres) {
+        float q[VEC];
+        Elem<T>::unpack(rr[c], q);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] += q[k];
+      }
+      store_place<T, ALIGNED>(static_cast<T*>(a.dx) + base, p, c, Elem<T>::pack(o));
+    }
+    if (PF) {
+#pragma unroll
+      for (int c = 0; c < VPT; ++c) {
+        rh[c] = nh[c];
+        rd[c] = nd[c];
+      }
+    }
+  }
+  if (partial == nullptr) return;
+  float* out = partial + static_cast<size_t>(blockIdx.x / TEAMS) * a.cols;
+  if constexpr (WARP) {
+    __shared__ float sums[MAXT / 32][32 * EPT];
+#pragma unroll
+    for (int c = 0; c < VPT; ++c)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const int e = col_at<VEC, ALIGNED>(p, c, k);
+        if (e < cols) sums[warp][e] = acc[c * VEC + k];
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < cols; e += blockDim.x) {
+      float v = sums[0][e];
+      for (int w = 1; w < warps; ++w) v += sums[w][e];
+      out[e] = v;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const int e = col_at<VEC, ALIGNED>(p, c, k);
+        if (e < cols) out[e] = acc[c * VEC + k];
+      }
+  }
+}
 
 // ---------------------------------------------------------------- streaming path
 
@@ -69,14 +223,33 @@ __global__ void __launch_bounds__(kColThreads)
   partial[blockIdx.y * a.cols + j] = acc;
 }
 
-// dgamma_j = sum of the groups' partial sums, in order.
-__global__ void __launch_bounds__(kColThreads)
+// dgamma_j = sum of the groups' partial sums: 32 columns per block, every
+// 16th group to each of its 16 warps, the warps' sums added in order.
+__global__ void __launch_bounds__(kJoinCols* kJoinWays)
     rmsnorm_bwd_join_kernel(const float* partial, float* dgamma, size_t cols, size_t groups) {
-  const size_t j = static_cast<size_t>(blockIdx.x) * kColThreads + threadIdx.x;
-  if (j >= cols) return;
+  __shared__ float part[kJoinWays][kJoinCols];
+  const int lane = threadIdx.x % kJoinCols, way = threadIdx.x / kJoinCols;
+  const size_t j = static_cast<size_t>(blockIdx.x) * kJoinCols + lane;
   float acc = 0.0f;
-  for (size_t g = 0; g < groups; ++g) acc += partial[g * cols + j];
-  dgamma[j] = acc;
+  if (j < cols) {
+#pragma unroll 4
+    for (size_t g = way; g < groups; g += kJoinWays) acc += partial[g * cols + j];
+  }
+  part[way][lane] = acc;
+  __syncthreads();
+  if (way == 0 && j < cols) {
+#pragma unroll
+    for (int w = 1; w < kJoinWays; ++w) acc += part[w][lane];
+    dgamma[j] = acc;
+  }
+}
+
+cudaError_t launch_join(const float* partial, float* dgamma, size_t cols, size_t groups, cudaStream_t s) {
+  const size_t blocks = (cols + kJoinCols - 1) / kJoinCols;
+  if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
+  rmsnorm_bwd_join_kernel<<<static_cast<unsigned>(blocks), kJoinCols * kJoinWays, 0, s>>>(partial, dgamma, cols,
+                                                                                      groups);
+  return cudaGetLastError();
 }
 
 // dx, elementwise once the statistics stand (after the column sums have read
@@ -115,21 +288,91 @@ cudaError_t launch_stream(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(used));
     rmsnorm_bwd_cols_kernel<T><<<grid, kColThreads, 0, s>>>(a, stats, partial, per);
-    rmsnorm_bwd_join_kernel<<<grid.x, kColThreads, 0, s>>>(partial, a.dgamma, a.cols, used);
+    const cudaError_t e = launch_join(partial, a.dgamma, a.cols, used, s);
+    if (e != cudaSuccess) return e;
   }
   rmsnorm_bwd_dx_kernel<T><<<g, kStreamThreads, 0, s>>>(a, stats);
   return cudaGetLastError();
+}
+
+// How the registers-resident kernel is launched for a shape: blocks, threads,
+// blocks per team, rows of partial sums.
+struct BwdLaunch {
+  int ept, cluster, threads;
+  size_t blocks, groups;
+};
+
+// Teams stay resident: as many blocks as fit the registers (128 a thread).
+BwdLaunch bwd_launch(size_t rows, size_t cols) {
+  BwdLaunch l;
+  if (cols <= static_cast<size_t>(kRowWarpCols)) {
+    // a warp per row, 8 / 16 / 32 values a lane (about 80 / 110 / 200 registers: 3 / 2 / 1 blocks per SM)
+    l.ept = cols <= 256 ? 8 : cols <= 512 ? 16 : 32;
+    l.cluster = 0;
+    l.threads = 32 * kRowWarps;
+    const size_t fit = kSmCount * (l.ept == 8 ? 3 : l.ept == 16 ? 2 : 1), want = (rows + kRowWarps - 1) / kRowWarps;
+    l.blocks = l.groups = want < fit ? want : fit;
+    return l;
+  }
+  l.ept = kBwdEpt;
+  l.cluster = cols <= kBwdBlockCols ? 1 : cols <= 2 * kBwdBlockCols ? 2 : 4;
+  const size_t per = kBwdEpt * static_cast<size_t>(l.cluster);
+  l.threads = static_cast<int>(((cols + per - 1) / per + 31) / 32 * 32);
+  const size_t fit = kSmCount / l.cluster * (l.cluster == 1 ? kBwdThreads / l.threads : 1);
+  l.groups = rows < fit ? rows : fit;
+  l.blocks = l.groups * l.cluster;
+  return l;
+}
+
+template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
+cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(l.blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(l.threads));
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CL > 1 ? CL : 1;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, ALIGNED, MAXT>, a, partial);
+}
+
+template <typename T, bool ALIGNED>
+cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
+  const BwdLaunch l = bwd_launch(a.rows, a.cols);
+  float* partial = a.dgamma ? static_cast<float*>(ws) : nullptr;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (l.cluster == 0) {
+    if (l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 0, 256>(a, partial, l, s);
+    if (l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 0, 256>(a, partial, l, s);
+    if (l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 0, 256>(a, partial, l, s);
+  } else {
+    if (l.cluster == 1) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 1, kBwdThreads>(a, partial, l, s);
+    if (l.cluster == 2) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 2, kBwdThreads>(a, partial, l, s);
+    if (l.cluster == 4) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 4, kBwdThreads>(a, partial, l, s);
+  }
+  if (e != cudaSuccess || partial == nullptr) return e;
+  return launch_join(partial, a.dgamma, a.cols, l.groups, s);
+}
+
+template <typename T>
+cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
+  if (a.cols > 4 * kBwdBlockCols) return launch_stream<T>(a, ws, s);
+  return a.aligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
 }
 
 }  // namespace
 
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
   (void)dtype;
-  return stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
+  if (cols > 4 * kBwdBlockCols) return stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
+  return want_dgamma ? bwd_launch(rows, cols).groups * cols * sizeof(float) : 0;
 }
 
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, void* ws, cudaStream_t stream) {
-  return a.dtype == FK_F32 ? launch_stream<float>(a, ws, stream) : launch_stream<__nv_bfloat16>(a, ws, stream);
+  return a.dtype == FK_F32 ? launch_type<float>(a, ws, stream) : launch_type<__nv_bfloat16>(a, ws, stream);
 }
 
 }  // namespace fk
