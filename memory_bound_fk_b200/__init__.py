@@ -381,9 +381,18 @@ def make_plan(path: int, threads: int = 0, vpt: int = 0, cluster: int = 0, chunk
 
 # ---------------------------------------------------------------- tensors
 
+_raw_stream = None     # torch's current-stream lookup by device index, found at first use
+
+
 def _stream_handle(t) -> int:
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # the handle itself, without building a Stream object around it
+        # (2.4 us); older or newer torch may not have it under this name
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def _check_tensor(t, name: str):
@@ -570,14 +579,14 @@ def _q8_code(dt):
     return _Q8_TYPES.get(dt)
 
 
-def _like(t, name: str, shape, dtype, device) -> int:
+def _like(t, name: str, shape, dtype, device: int) -> int:
     """Address of an operand that must be contiguous CUDA memory of this
-    shape, type and device (0 for None)."""
+    shape, type and device index (0 for None)."""
     if t is None:
         return 0
     _check_tensor(t, name)
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must have shape {tuple(shape)} and type {dtype}, on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} and type {dtype}, on cuda:{device}")
     return t.data_ptr()
 
 
@@ -601,12 +610,13 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out_dtype=None, ou
     import torch
     _check_tensor(x, "x")
     code = _dtype_code(x.dtype)
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
     rows, cols = _rows_of(x, "x")
-    dev = x.device
+    lead = shape[:-1]
     if out_dtype is None:
-        out_dtype = x.dtype if out is None else out.dtype
+        out_dtype = dtype if out is None else out.dtype
     q8 = _q8_code(out_dtype)
-    if q8 is None and out_dtype != x.dtype:
+    if q8 is None and out_dtype != dtype:
         raise TypeError("out_dtype must be x's dtype, torch.int8 or torch.float8_e4m3fn")
     if q8 is None and scales is not None:
         raise ValueError("scales belong to 8-bit outputs")
@@ -614,18 +624,25 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out_dtype=None, ou
         raise ValueError("rows without columns have no scale")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out needs a residual")
+    # what is made here needs no checks
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        out = torch.empty_like(x, dtype=out_dtype)
+        p_out = out.data_ptr()
+    else:
+        p_out = _like(out, "out", shape, out_dtype, dev)
     if q8 is not None and scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        scales = x.new_empty(lead, dtype=torch.float32)
+        p_scales = scales.data_ptr()
+    else:
+        p_scales = _like(scales, "scales", lead, torch.float32, dev)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(x)
-    st = lib().fk_rmsnorm_rows(x.data_ptr(), _like(residual, "residual", x.shape, x.dtype, dev),
-                               _like(weight, "weight", (cols,), torch.float32, dev),
-                               _like(out, "out", x.shape, out_dtype, dev),
-                               _like(scales, "scales", x.shape[:-1], torch.float32, dev),
-                               _like(residual_out, "residual_out", x.shape, x.dtype, dev), rows, cols, code,
-                               code if q8 is None else q8, eps, _stream_handle(x))
+        p_h = residual_out.data_ptr()
+    else:
+        p_h = _like(residual_out, "residual_out", shape, dtype, dev)
+    st = lib().fk_rmsnorm_rows(x.data_ptr(), _like(residual, "residual", shape, dtype, dev),
+                               _like(weight, "weight", (cols,), torch.float32, dev), p_out, p_scales, p_h, rows, cols,
+                               code, code if q8 is None else q8, eps, _stream_handle(x))
     if st != FK_OK:
         raise FkError(st, "fk_rmsnorm_rows")
     if q8 is None:
@@ -647,19 +664,19 @@ def rmsnorm_backward(dy, h, weight=None, eps: float = 1e-6, dresidual=None, out=
     _check_tensor(h, "h")
     code = _dtype_code(h.dtype)
     rows, cols = _rows_of(h, "h")
-    dev = h.device
+    shape, dtype, dev = h.shape, h.dtype, h.get_device()
     if not need_dweight:
         if dweight is not None:
             raise ValueError("dweight given, but need_dweight is false")
     elif dweight is None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+        dweight = h.new_empty((cols,), dtype=torch.float32)
     if out is None:
         out = torch.empty_like(h)
     if dy is None:
         raise TypeError("dy must be a CUDA tensor")
-    args = (_like(dy, "dy", h.shape, h.dtype, dev), h.data_ptr(),
-            _like(weight, "weight", (cols,), torch.float32, dev), _like(dresidual, "dresidual", h.shape, h.dtype, dev),
-            _like(out, "out", h.shape, h.dtype, dev), _like(dweight, "dweight", (cols,), torch.float32, dev), rows,
+    args = (_like(dy, "dy", shape, dtype, dev), h.data_ptr(),
+            _like(weight, "weight", (cols,), torch.float32, dev), _like(dresidual, "dresidual", shape, dtype, dev),
+            _like(out, "out", shape, dtype, dev), _like(dweight, "dweight", (cols,), torch.float32, dev), rows,
             cols, code, eps)
     if workspace is None:
         st = lib().fk_rmsnorm_rows_bwd(*args, _stream_handle(h))
@@ -692,11 +709,13 @@ def quantize_rows(x, dtype=None, gelu: str | None = None, out=None, scales=None)
     if q8 is None:
         raise TypeError("dtype must be torch.int8 or torch.float8_e4m3fn")
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+        out = torch.empty_like(x, dtype=dtype)
+    shape, dev = x.shape, x.get_device()
+    lead = shape[:-1]
     if scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    st = lib().fk_quantize_rows(x.data_ptr(), _like(out, "out", x.shape, dtype, x.device),
-                                _like(scales, "scales", x.shape[:-1], torch.float32, x.device), rows, cols, code, q8,
+        scales = x.new_empty(lead, dtype=torch.float32)
+    st = lib().fk_quantize_rows(x.data_ptr(), _like(out, "out", shape, dtype, dev),
+                                _like(scales, "scales", lead, torch.float32, dev), rows, cols, code, q8,
                                 _EPILOGUES[gelu], _stream_handle(x))
     if st != FK_OK:
         raise FkError(st, "fk_quantize_rows")
@@ -718,18 +737,18 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, gelu: str | None = None, out_
     q8 = _q8_code(a.dtype)
     if q8 is None or b.dtype != a.dtype:
         raise TypeError("a and b must both be torch.int8 or both torch.float8_e4m3fn")
-    if a.dim() == 0 or b.dim() != 2 or b.shape[1] != a.shape[-1] or b.device != a.device:
+    if a.dim() == 0 or b.dim() != 2 or b.shape[1] != a.shape[-1] or b.get_device() != a.get_device():
         raise ValueError("a is [..., k] and b is [n, k], on one device")
     if gelu not in _EPILOGUES:
         raise ValueError("gelu must be None, 'tanh' or 'erf'")
     n, k = b.shape
-    lead, dev = a.shape[:-1], a.device
+    lead, dev = a.shape[:-1], a.get_device()
     if a_scales is None or b_scales is None:
         raise TypeError("a_scales and b_scales must be CUDA tensors")
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
     if out is None:
-        out = torch.empty((*lead, n), dtype=out_dtype, device=dev)
+        out = a.new_empty((*lead, n), dtype=out_dtype)
     m = lead.numel()
     args = (a.data_ptr(), b.data_ptr(), _like(a_scales, "a_scales", lead, torch.float32, dev),
             _like(b_scales, "b_scales", (n,), torch.float32, dev), _like(bias, "bias", (n,), torch.float32, dev),
