@@ -18,25 +18,16 @@
 
 #include "fk_common.cuh"
 #include "fk_mm.cuh"
+#include "fk_mm_host.h"
 #include "fk_q8_internal.h"
 
 namespace fk {
 namespace {
 
 constexpr int kChan = 128;   // channels per tile (MMA M)
-constexpr int kKBlock = 128; // codes of k per stage (one swizzled row)
+using mm::kKBlock;
 constexpr int kMmThreads = 192;  // four epilogue warps, the load warp, the MMA warp
 constexpr size_t kMaxGrid = 0x7fffffffu;
-
-struct MmParams {
-  const float* sa;
-  const float* sb;
-  const float* bias;
-  void* c;
-  int m, n;
-  int kblocks;  // ceil(k / 128)
-  int tiles_n;  // ceil(n / 128)
-};
 
 // ---------------------------------------------------------------- one tile per block, k split over a cluster
 
@@ -58,7 +49,7 @@ struct SplitShape {
 template <int Q8, int TN, int SPLIT, typename T, int EPI>
 __global__ void __launch_bounds__(kMmThreads)
     matmul_split_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
-                        MmParams p) {
+                        mm::Params p) {
   using S = SplitShape<TN>;
   constexpr int ST = S::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -257,43 +248,21 @@ PFN_encodeTiled encode_fn() {
   return fn;
 }
 
-// [rows, k] codes with a row pitch of `pitch` bytes (a multiple of 16), in
-// boxes of 128 codes x box_rows rows, 128-byte swizzle; outside reads 0.
-bool make_map(CUtensorMap* m, const void* ptr, size_t rows, size_t k, size_t pitch, int box_rows) {
-  PFN_encodeTiled f = encode_fn();
-  if (f == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  const cuuint32_t box[2] = {kKBlock, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A product whose operands TMA can read.
-struct MmCall {
-  const void *a, *b;
-  size_t k, pitch;
-  MatmulQ8Args p;
-  int sm_count;
-  cudaStream_t stream;
-};
-
 template <int Q8, int TN, int SPLIT, typename T, int EPI>
-cudaError_t launch_split(const MmCall& c) {
+cudaError_t launch_split(const mm::Call& c) {
   using S = SplitShape<TN>;
   const size_t tiles_n = (c.p.n + kChan - 1) / kChan, tiles_m = (c.p.m + TN - 1) / TN;
   if (tiles_m > kMaxGrid / SPLIT / tiles_n) return cudaErrorInvalidConfiguration;
   CUtensorMap ma, mb;
-  if (!make_map(&ma, c.a, c.p.m, c.k, c.pitch, TN) || !make_map(&mb, c.b, c.p.n, c.k, c.pitch, kChan))
+  if (!mm::make_map(&ma, c.a, c.p.m, c.k, c.pitch, TN) || !mm::make_map(&mb, c.b, c.p.n, c.k, c.pitch, kChan))
     return cudaErrorInvalidValue;
   const size_t smem = S::kStages * S::kStageBytes + (SPLIT > 1 ? S::kRedBytes : 0) + 1024;
   auto kernel = matmul_split_kernel<Q8, TN, SPLIT, T, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  MmParams p = {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m), static_cast<int>(c.p.n),
-                static_cast<int>((c.k + kKBlock - 1) / kKBlock), static_cast<int>(tiles_n)};
+  const mm::Params p = {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m),
+                        static_cast<int>(c.p.n), static_cast<int>((c.k + kKBlock - 1) / kKBlock),
+                        static_cast<int>(tiles_n), static_cast<int>(tiles_m)};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles_n * tiles_m * SPLIT));
   cfg.blockDim = dim3(kMmThreads);
@@ -311,7 +280,7 @@ cudaError_t launch_split(const MmCall& c) {
 // Blocks of a cluster that share a tile: doubled while the grid still fits
 // two blocks per SM at once and each keeps at least four 128-code steps of k.
 template <int Q8, int TN, typename T, int EPI>
-cudaError_t launch_tokens(const MmCall& c) {
+cudaError_t launch_tokens(const mm::Call& c) {
   const size_t tiles = ((c.p.n + kChan - 1) / kChan) * ((c.p.m + TN - 1) / TN);
   const size_t kblocks = (c.k + kKBlock - 1) / kKBlock, room = 2 * static_cast<size_t>(c.sm_count);
   int split = 1;
@@ -325,7 +294,7 @@ cudaError_t launch_tokens(const MmCall& c) {
 }
 
 template <int Q8, typename T, int EPI>
-cudaError_t launch_epi(const MmCall& c) {
+cudaError_t launch_epi(const mm::Call& c) {
   if (c.p.m <= 16) return launch_tokens<Q8, 16, T, EPI>(c);
   if (c.p.m <= 32) return launch_tokens<Q8, 32, T, EPI>(c);
   if (c.p.m <= 64) return launch_tokens<Q8, 64, T, EPI>(c);
@@ -333,7 +302,7 @@ cudaError_t launch_epi(const MmCall& c) {
 }
 
 template <int Q8, typename T>
-cudaError_t launch_out(const MmCall& c) {
+cudaError_t launch_out(const mm::Call& c) {
   switch (c.p.epilogue) {
     case FK_EPILOGUE_GELU_TANH: return launch_epi<Q8, T, FK_EPILOGUE_GELU_TANH>(c);
     case FK_EPILOGUE_GELU_ERF: return launch_epi<Q8, T, FK_EPILOGUE_GELU_ERF>(c);
@@ -342,7 +311,7 @@ cudaError_t launch_out(const MmCall& c) {
 }
 
 template <int Q8>
-cudaError_t launch_type(const MmCall& c) {
+cudaError_t launch_type(const mm::Call& c) {
   return c.p.out_dtype == FK_F32 ? launch_out<Q8, float>(c) : launch_out<Q8, __nv_bfloat16>(c);
 }
 
@@ -357,12 +326,26 @@ cudaError_t launch_pad(const void* src, void* dst, size_t rows, size_t k, cudaSt
 
 }  // namespace
 
+namespace mm {
+bool make_map(CUtensorMap* m, const void* ptr, size_t rows, size_t k, size_t pitch, int box_rows) {
+  PFN_encodeTiled f = encode_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  const cuuint32_t box[2] = {kKBlock, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace mm
+
 size_t matmul_q8_workspace(size_t m, size_t n, size_t k, bool aligned) {
   return aligned && k % 16 == 0 ? 0 : (m + n) * round16(k);
 }
 
 cudaError_t launch_matmul_q8(const MatmulQ8Args& p, void* ws, int sm_count, cudaStream_t s) {
-  MmCall c = {p.a, p.b, p.k, p.k, p, sm_count > 0 ? sm_count : 1, s};
+  mm::Call c = {p.a, p.b, p.k, p.k, p, sm_count > 0 ? sm_count : 1, s};
   if (ws != nullptr) {
     // operands that TMA cannot read as they are
     const size_t kp = round16(p.k);
@@ -379,6 +362,7 @@ cudaError_t launch_matmul_q8(const MatmulQ8Args& p, void* ws, int sm_count, cuda
     }
     c.k = c.pitch = kp;
   }
+  if (p.m > 256) return mm::launch_pair(c);
   return p.dtype == FK_I8 ? launch_type<FK_I8>(c) : launch_type<FK_E4M3>(c);
 }
 
@@ -388,6 +372,9 @@ cudaError_t read_matmul_wait_timeouts(unsigned* out, bool reset) {
     const unsigned zero = 0;
     e = cudaMemcpyToSymbol(mm::g_mm_wait_timeouts, &zero, sizeof(unsigned));
   }
+  unsigned pair = 0;
+  if (e == cudaSuccess) e = mm::read_pair_wait_timeouts(&pair, reset);
+  *out += pair;
   return e;
 }
 

@@ -1,0 +1,44 @@
+// fk_mm_host.h -- host side shared by the kernels of the 8-bit product: the
+// launch parameters and the TMA tensor maps.  Not installed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fk_q8_internal.h"
+
+namespace fk {
+namespace mm {
+
+constexpr int kKBlock = 128;  // codes of k per stage (one swizzled row)
+
+struct Params {
+  const float* sa;
+  const float* sb;
+  const float* bias;
+  void* c;
+  int m, n;
+  int kblocks;  // ceil(k / 128)
+  int tiles_n, tiles_m;
+};
+
+// A product whose operands TMA can read: [m, k] and [n, k] with a row pitch
+// that is a multiple of 16 bytes.
+struct Call {
+  const void *a, *b;
+  size_t k, pitch;
+  MatmulQ8Args p;
+  int sm_count;
+  cudaStream_t stream;
+};
+
+// [rows, k] codes in boxes of 128 codes x box_rows rows, 128-byte swizzle;
+// outside reads 0.
+bool make_map(CUtensorMap* m, const void* ptr, size_t rows, size_t k, size_t pitch, int box_rows);
+
+// The kernel for many tokens (fk_matmul_q8_pair.cu).
+cudaError_t launch_pair(const Call& c);
+cudaError_t read_pair_wait_timeouts(unsigned* out, bool reset);
+
+}  // namespace mm
+}  // namespace fk
