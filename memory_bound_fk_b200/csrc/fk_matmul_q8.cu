@@ -11,6 +11,9 @@
 // and the tensor maps fill what lies outside [m, k] and [n, k] with zeros, so
 // ragged edges need no code in the main loop.
 //
+// This file: up to 64 tokens, one tile per block with k split over a cluster.
+// More tokens: fk_matmul_q8_pair.cu.
+//
 // The product is bound by reading B once while m is below about 250 (B at
 // 6.5 TB/s against 2 m ops a byte at 3.4 POP/s), by the tensor cores above.
 #include <cuda.h>
@@ -19,6 +22,7 @@
 #include "fk_common.cuh"
 #include "fk_mm.cuh"
 #include "fk_mm_host.h"
+#include "fk_q8.cuh"
 #include "fk_q8_internal.h"
 
 namespace fk {
@@ -27,6 +31,7 @@ namespace {
 constexpr int kChan = 128;   // channels per tile (MMA M)
 using mm::kKBlock;
 constexpr int kMmThreads = 192;  // four epilogue warps, the load warp, the MMA warp
+constexpr size_t kMaxTokens = 64;  // more go to the pairs of SMs (fk_matmul_q8_pair.cu)
 constexpr size_t kMaxGrid = 0x7fffffffu;
 
 // ---------------------------------------------------------------- one tile per block, k split over a cluster
@@ -40,9 +45,11 @@ template <int TN>
 struct SplitShape {
   static constexpr uint32_t kStageBytes = (kChan + TN) * kKBlock;
   static constexpr uint32_t kRedBytes = TN * kChan * 4;
-  // about 96 KB of stages, so that two blocks fit an SM: 2 x 96 KB in flight
-  // is more than the 54 KB an SM needs to cover HBM latency at full rate
-  static constexpr int kStages = TN >= 128 ? 3 : TN >= 64 ? 4 : 5;
+  // stages and partials together stay below half an SM's shared memory, so
+  // that two blocks fit and one's start and end hide under the other's loads
+  // (2 x 72 to 96 KB in flight; covering HBM latency at full rate takes 54)
+  static constexpr int kStages = TN >= 64 ? 3 : TN >= 32 ? 4 : 5;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kRedBytes;
   static constexpr uint32_t kTmemCols = TN < 32 ? 32 : TN;
 };
 
@@ -80,10 +87,11 @@ __global__ void __launch_bounds__(kMmThreads)
     abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (tid < TN) s_sa[tid] = m0 + tid < p.m ? p.sa[m0 + tid] : 0.0f;
+  let_next_start();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  after_previous();
   if constexpr (SPLIT > 1) cluster_arrive_relaxed();  // every block of the cluster has started: waited for below
   const uint32_t tmem = tmem_slot;
 
@@ -121,21 +129,23 @@ __global__ void __launch_bounds__(kMmThreads)
     }
     __syncwarp();
   }
-  if constexpr (SPLIT > 1) cluster_wait();
-
-  // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, lane = channel
+  // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, lane = channel; the
+  // scales are fetched while the MMAs run
+  const int chan = n0 + tid;
+  float sb = 0.0f, bias = 0.0f;
   if (warp < 4) {
+    if (tid < TN) s_sa[tid] = m0 + tid < p.m ? p.sa[m0 + tid] : 0.0f;
+    if (chan < p.n) {
+      sb = p.sb[chan];
+      bias = p.bias ? p.bias[chan] : 0.0f;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // s_sa stands
     mm::drain(&done, 0);
     tc::fence_after_sync();
   }
-  const int chan = n0 + tid;
+  if constexpr (SPLIT > 1) cluster_wait();
   const bool good = *abort == 0;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-  float sb = 0.0f, bias = 0.0f;
-  if (warp < 4 && chan < p.n) {
-    sb = p.sb[chan];
-    bias = p.bias ? p.bias[chan] : 0.0f;
-  }
   T* c = static_cast<T*>(p.c);
   auto finish = [&](uint32_t w, int t) {
     const float v = mm::act<EPI>(mm::acc_value<Q8>(w) * s_sa[t] * sb + bias);
@@ -194,6 +204,8 @@ __global__ void __launch_bounds__(kMmThreads)
 // funnel shift, or single bytes next to the ends of src.
 __global__ void __launch_bounds__(256)
     matmul_pad_kernel(const uint8_t* src, uint4* dst, size_t rows, size_t k, size_t chunks) {
+  let_next_start();
+  after_previous();
   const size_t total = rows * chunks, end = rows * k;
   for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
        i += static_cast<size_t>(gridDim.x) * 256) {
@@ -256,35 +268,28 @@ cudaError_t launch_split(const mm::Call& c) {
   CUtensorMap ma, mb;
   if (!mm::make_map(&ma, c.a, c.p.m, c.k, c.pitch, TN) || !mm::make_map(&mb, c.b, c.p.n, c.k, c.pitch, kChan))
     return cudaErrorInvalidValue;
-  const size_t smem = S::kStages * S::kStageBytes + (SPLIT > 1 ? S::kRedBytes : 0) + 1024;
+  const size_t smem = S::kSmem;
   auto kernel = matmul_split_kernel<Q8, TN, SPLIT, T, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const mm::Params p = {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m),
                         static_cast<int>(c.p.n), static_cast<int>((c.k + kKBlock - 1) / kKBlock),
                         static_cast<int>(tiles_n), static_cast<int>(tiles_m)};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles_n * tiles_m * SPLIT));
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = c.stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = SPLIT;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = SPLIT > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+  return launch_overlapped(kernel, static_cast<unsigned>(tiles_n * tiles_m * SPLIT), kMmThreads, smem, SPLIT, c.stream,
+                           ma, mb, p);
 }
 
 // Blocks of a cluster that share a tile: doubled while the grid still fits
-// two blocks per SM at once and each keeps at least four 128-code steps of k.
+// two blocks per SM at once and each keeps two 128-code steps of k.  Measured
+// on B200 in a captured chain (one token, int8, us for 1 / 2 / 4 / 8 blocks a
+// tile): 1024 x 1024 4.3 / 3.5 / 3.0 / 2.8; 4096 x 4096 12.4 / 7.9 / 6.3 / 6.3;
+// 8192 x 8192 22.3 / 14.7 / 14.1 / 16.6; 16384 x 4096 14.6 / 14.4 / 16.0 / 20.7.
 template <int Q8, int TN, typename T, int EPI>
 cudaError_t launch_tokens(const mm::Call& c) {
   const size_t tiles = ((c.p.n + kChan - 1) / kChan) * ((c.p.m + TN - 1) / TN);
   const size_t kblocks = (c.k + kKBlock - 1) / kKBlock, room = 2 * static_cast<size_t>(c.sm_count);
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= room && kblocks >= static_cast<size_t>(split) * 2 * 4) split *= 2;
+  while (split < 8 && tiles * split * 2 <= room && kblocks >= static_cast<size_t>(split) * 4) split *= 2;
   switch (split) {
     case 1: return launch_split<Q8, TN, 1, T, EPI>(c);
     case 2: return launch_split<Q8, TN, 2, T, EPI>(c);
@@ -297,8 +302,7 @@ template <int Q8, typename T, int EPI>
 cudaError_t launch_epi(const mm::Call& c) {
   if (c.p.m <= 16) return launch_tokens<Q8, 16, T, EPI>(c);
   if (c.p.m <= 32) return launch_tokens<Q8, 32, T, EPI>(c);
-  if (c.p.m <= 64) return launch_tokens<Q8, 64, T, EPI>(c);
-  return launch_tokens<Q8, 128, T, EPI>(c);
+  return launch_tokens<Q8, 64, T, EPI>(c);
 }
 
 template <int Q8, typename T>
@@ -319,9 +323,8 @@ size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 
 cudaError_t launch_pad(const void* src, void* dst, size_t rows, size_t k, cudaStream_t s) {
   const size_t chunks = round16(k) / 16, blocks = (rows * chunks + 255) / 256;
-  matmul_pad_kernel<<<static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, s>>>(
-      static_cast<const uint8_t*>(src), static_cast<uint4*>(dst), rows, k, chunks);
-  return cudaGetLastError();
+  return launch_overlapped(matmul_pad_kernel, static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, 1, s,
+                           static_cast<const uint8_t*>(src), static_cast<uint4*>(dst), rows, k, chunks);
 }
 
 }  // namespace
@@ -362,7 +365,10 @@ cudaError_t launch_matmul_q8(const MatmulQ8Args& p, void* ws, int sm_count, cuda
     }
     c.k = c.pitch = kp;
   }
-  if (p.m > 256) return mm::launch_pair(c);
+  // Past 64 tokens the pairs of SMs win (128 tokens, 4096 x 4096: 10.9 us
+  // against 12.6 with 128-token tiles here); at 64 and below these kernels do
+  // (64 tokens, 4096 x 4096: 8.5 against 10.9; 16384 x 4096 17.4 against 16.2).
+  if (p.m > kMaxTokens) return mm::launch_pair(c);
   return p.dtype == FK_I8 ? launch_type<FK_I8>(c) : launch_type<FK_E4M3>(c);
 }
 

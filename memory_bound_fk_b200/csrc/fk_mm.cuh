@@ -95,12 +95,13 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint6
 }
 
 // One arrival on the barrier at this offset in both blocks of the pair when
-// every MMA issued before by this thread has completed.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// every MMA issued before by this thread has completed.  `leader`: the
+// issuing block's rank in its cluster (even).
+__device__ __forceinline__ void commit_pair(uint64_t* bar, int leader) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_addr(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3 << leader))
       : "memory");
 }
 
@@ -145,8 +146,19 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The arrival alone, with release (cluster_wait() completes it).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
 }
 
 // Accumulator word to fp32: the exact integer sum rounded once, or the sum.

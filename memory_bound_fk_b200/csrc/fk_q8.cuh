@@ -18,6 +18,14 @@ namespace {
 
 constexpr float kTinyAmax = 0x1p-100f;
 
+// Programmatic dependent launch: a kernel launched with overlap allowed
+// (launch_overlapped) may start while its predecessor in the stream still
+// runs.  after_previous() returns once the predecessor has completed and its
+// writes are visible; nothing in global memory is touched before it.
+// let_next_start() allows the same to the successor.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // max(a, |b|), NaN if either is.
 __device__ __forceinline__ float absmax_nan(float a, float b) {
   float r;

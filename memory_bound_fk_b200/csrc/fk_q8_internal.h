@@ -20,6 +20,28 @@ fk_status validate_span(const void* p, size_t bytes, size_t align);
 // cudaSuccess).
 fk_status report_cuda(cudaError_t e);
 
+// Launch a kernel that calls after_previous() before it touches global
+// memory: its start (launch latency, barriers, tensor memory) overlaps the
+// end of the kernel before it in the stream.  cluster: blocks per cluster.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(KArgs...), unsigned grid, unsigned threads, size_t smem,
+                              unsigned cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- RMSNorm ---------------------------------------------------------------
 // Validated arguments of fk_rmsnorm_rows.  `aligned`: every row of x,
 // residual, h and y (and gamma) allows 16-byte vector access (8- or 4-byte

@@ -35,6 +35,8 @@ template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, bool WARP, int MA
 __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(QuantizeArgs a) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   __shared__ float2 red[WARP ? 1 : MAXT / 32];
+  let_next_start();
+  after_previous();
   for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, const Place& p) {
     const size_t base = row * a.cols;
     uint4 raw[VPT];
@@ -68,6 +70,8 @@ template <typename T, int OUT, int EPI>
 __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(QuantizeArgs a) {
   __shared__ float2 red[kStreamThreads / 32];
   const size_t cols = a.cols;
+  let_next_start();
+  after_previous();
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * cols;
     uint8_t* o = static_cast<uint8_t*>(a.q) + row * cols;
@@ -83,24 +87,24 @@ __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(Quantiz
 }
 
 template <typename T, int OUT, int EPI, bool ALIGNED>
-void launch_rows(const QuantizeArgs& a, cudaStream_t s) {
+cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
   if (a.cols <= kRowWarpCols) {
     const RowLaunch l = warp_launch(a.rows);
     if (a.cols <= kRowWarpCols / 4)
-      quantize_row_kernel<T, OUT, EPI, 8, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 8, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
     else if (a.cols <= kRowWarpCols / 2)
-      quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
     else
-      quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   } else if (a.cols <= kRowSmallCols) {
     const RowLaunch l = block_launch(a.rows, a.cols, 16);
-    quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else if (a.cols <= kRowLargeCols) {
     const RowLaunch l = block_launch(a.rows, a.cols, 32);
-    quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else {
     const RowLaunch l = block_launch(a.rows, a.cols, 32);
-    quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 1024, 1><<<l.grid, l.threads, 0, s>>>(a);
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
   }
 }
 
@@ -108,13 +112,9 @@ template <typename T, int OUT, int EPI>
 cudaError_t launch_epi(const QuantizeArgs& a, cudaStream_t s) {
   if (a.cols > kRowMaxCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
-    quantize_stream_kernel<T, OUT, EPI><<<g, kStreamThreads, 0, s>>>(a);
-  } else if (a.aligned) {
-    launch_rows<T, OUT, EPI, true>(a, s);
-  } else {
-    launch_rows<T, OUT, EPI, false>(a, s);
+    return launch_overlapped(quantize_stream_kernel<T, OUT, EPI>, g, kStreamThreads, 0, 1, s, a);
   }
-  return cudaGetLastError();
+  return a.aligned ? launch_rows<T, OUT, EPI, true>(a, s) : launch_rows<T, OUT, EPI, false>(a, s);
 }
 
 template <typename T, int OUT>

@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(RmsnormArgs a) 
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   __shared__ float2 red[WARP ? 1 : MAXT / 32];
   const float inv_n = 1.0f / static_cast<float>(a.cols);
+  let_next_start();
+  after_previous();
   for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, const Place& p) {
     const size_t base = row * a.cols;
     uint4 raw[VPT];
@@ -98,6 +100,8 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
   __shared__ float2 red[kStreamThreads / 32];
   const size_t cols = a.cols;
   const float inv_n = 1.0f / static_cast<float>(cols);
+  let_next_start();
+  after_previous();
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * cols;
     const T* r = a.residual ? static_cast<const T*>(a.residual) + row * cols : nullptr;
@@ -138,24 +142,24 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
 }
 
 template <typename T, int OUT, bool ALIGNED>
-void launch_rows(const RmsnormArgs& a, cudaStream_t s) {
+cudaError_t launch_rows(const RmsnormArgs& a, cudaStream_t s) {
   if (a.cols <= kRowWarpCols) {
     const RowLaunch l = warp_launch(a.rows);
     if (a.cols <= kRowWarpCols / 4)
-      rmsnorm_row_kernel<T, OUT, 8, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 8, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
     else if (a.cols <= kRowWarpCols / 2)
-      rmsnorm_row_kernel<T, OUT, 16, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
     else
-      rmsnorm_row_kernel<T, OUT, 32, ALIGNED, true, 32 * kRowWarps, 4><<<l.grid, l.threads, 0, s>>>(a);
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   } else if (a.cols <= kRowSmallCols) {
     const RowLaunch l = block_launch(a.rows, a.cols, 16);
-    rmsnorm_row_kernel<T, OUT, 16, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else if (a.cols <= kRowLargeCols) {
     const RowLaunch l = block_launch(a.rows, a.cols, 32);
-    rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 512, 2><<<l.grid, l.threads, 0, s>>>(a);
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else {
     const RowLaunch l = block_launch(a.rows, a.cols, 32);
-    rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 1024, 1><<<l.grid, l.threads, 0, s>>>(a);
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
   }
 }
 
@@ -163,13 +167,9 @@ template <typename T, int OUT>
 cudaError_t launch_out(const RmsnormArgs& a, cudaStream_t s) {
   if (a.cols > kRowMaxCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
-    rmsnorm_stream_kernel<T, OUT><<<g, kStreamThreads, 0, s>>>(a);
-  } else if (a.aligned) {
-    launch_rows<T, OUT, true>(a, s);
-  } else {
-    launch_rows<T, OUT, false>(a, s);
+    return launch_overlapped(rmsnorm_stream_kernel<T, OUT>, g, kStreamThreads, 0, 1, s, a);
   }
-  return cudaGetLastError();
+  return a.aligned ? launch_rows<T, OUT, true>(a, s) : launch_rows<T, OUT, false>(a, s);
 }
 
 template <typename T>

@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs
   const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps : gridDim.x / TEAMS;
   const T* const h = static_cast<const T*>(a.h);
   const T* const dy = static_cast<const T*>(a.dy);
+  let_next_start();
+  after_previous();
   if constexpr (CL > 1) cluster_arrive_relaxed();  // every block has started: waited for before the first push
   float gam[EPT], acc[EPT];
 #pragma unroll
@@ -231,6 +233,8 @@ __global__ void __launch_bounds__(kJoinCols* kJoinWays)
   const int lane = threadIdx.x % kJoinCols, way = threadIdx.x / kJoinCols;
   const size_t j = static_cast<size_t>(blockIdx.x) * kJoinCols + lane;
   float acc = 0.0f;
+  let_next_start();
+  after_previous();
   if (j < cols) {
 #pragma unroll 4
     for (size_t g = way; g < groups; g += kJoinWays) acc += partial[g * cols + j];
@@ -247,9 +251,8 @@ __global__ void __launch_bounds__(kJoinCols* kJoinWays)
 cudaError_t launch_join(const float* partial, float* dgamma, size_t cols, size_t groups, cudaStream_t s) {
   const size_t blocks = (cols + kJoinCols - 1) / kJoinCols;
   if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
-  rmsnorm_bwd_join_kernel<<<static_cast<unsigned>(blocks), kJoinCols * kJoinWays, 0, s>>>(partial, dgamma, cols,
-                                                                                      groups);
-  return cudaGetLastError();
+  return launch_overlapped(rmsnorm_bwd_join_kernel, static_cast<unsigned>(blocks), kJoinCols * kJoinWays, 0, 1, s,
+                           partial, dgamma, cols, groups);
 }
 
 // dx, elementwise once the statistics stand (after the column sums have read
@@ -326,17 +329,9 @@ BwdLaunch bwd_launch(size_t rows, size_t cols) {
 
 template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
 cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(l.blocks));
-  cfg.blockDim = dim3(static_cast<unsigned>(l.threads));
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CL > 1 ? CL : 1;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = CL > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, ALIGNED, MAXT>, a, partial);
+  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, ALIGNED, MAXT>,
+                           static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), 0, CL > 1 ? CL : 1, s, a,
+                           partial);
 }
 
 template <typename T, bool ALIGNED>
