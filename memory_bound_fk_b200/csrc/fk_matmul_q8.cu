@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kMmThreads)
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
   T* c = static_cast<T*>(p.c);
   auto finish = [&](uint32_t w, int t) {
-    const float v = mm::act<EPI>(mm::acc_value<Q8>(w) * s_sa[t] * sb + bias);
+    const float v = mm::act<EPI>(fmaf(mm::acc_value<Q8>(w) * s_sa[t], sb, bias));
     if (chan < p.n && m0 + t < p.m) c[static_cast<size_t>(m0 + t) * p.n + chan] = static_cast<T>(v);
   };
   if constexpr (SPLIT == 1) {

@@ -185,9 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         T* out = c + static_cast<size_t>(tok) * p.n + chan;
         const int left = p.m - tok;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const float v = act<EPI>(acc_value<Q8>(r[q]) * __shfl_sync(0xffffffffu, sa, q) * sb + bias);
-          if (in && q < left) *out = static_cast<T>(v);
+        for (int q = 0; q < 32; q += 2) {
+          const float2 v = finish2<Q8, EPI>(r[q], r[q + 1], __shfl_sync(0xffffffffu, sa, q),
+                                            __shfl_sync(0xffffffffu, sa, q + 1), sb, bias);
+          if (in && q < left) *out = static_cast<T>(v.x);
+          out += p.n;
+          if (in && q + 1 < left) *out = static_cast<T>(v.y);
           out += p.n;
         }
       }
@@ -355,9 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) sum[e] = o == 0 ? w[e] : acc_add<Q8>(sum[e], w[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = act<EPI>(acc_value<Q8>(sum[e]) * __shfl_sync(0xffffffffu, sa, q + e) * sb + bias);
-          if (in && q + e < left) *out = static_cast<T>(v);
+        for (int e = 0; e < 4; e += 2) {
+          const float2 v = finish2<Q8, EPI>(sum[e], sum[e + 1], __shfl_sync(0xffffffffu, sa, q + e),
+                                            __shfl_sync(0xffffffffu, sa, q + e + 1), sb, bias);
+          if (in && q + e < left) *out = static_cast<T>(v.x);
+          out += p.n;
+          if (in && q + e + 1 < left) *out = static_cast<T>(v.y);
           out += p.n;
         }
       }

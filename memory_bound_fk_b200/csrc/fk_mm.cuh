@@ -178,5 +178,16 @@ __device__ __forceinline__ float act(float x) {
   return x;
 }
 
+// act(acc * sa * sb + bias) of one channel for two tokens, packed: each lane
+// rounds as the scalar operations would.
+template <int Q8, int EPI>
+__device__ __forceinline__ float2 finish2(uint32_t w0, uint32_t w1, float sa0, float sa1, float sb, float bias) {
+  const float2 v = fma2(mul2(make_float2(acc_value<Q8>(w0), acc_value<Q8>(w1)), make_float2(sa0, sa1)), splat2(sb),
+                        splat2(bias));
+  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f2<float>(v);
+  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f2<float>(v);
+  return v;
+}
+
 }  // namespace mm
 }  // namespace fk

@@ -6,6 +6,7 @@
 #include <cfloat>
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "fk_q8_internal.h"
 
@@ -58,6 +59,22 @@ fk_status check_memory(const Span* s, int count) {
 bool shape_ok(size_t rows, size_t cols) { return rows <= SIZE_MAX / 8 / cols; }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// The mode of rows of `pitch` bytes in the given buffers (NULL ones aside);
+// parameters (and, for aligned rows, codes) sit on 16-byte boundaries.
+RowMode row_mode(size_t pitch, std::initializer_list<const void*> rows, const void* params, const void* codes) {
+  if (!aligned16(params)) return kRowsAny;
+  uintptr_t at = 0;
+  bool first = true;
+  for (const void* p : rows) {
+    if (p == nullptr) continue;
+    const uintptr_t off = reinterpret_cast<uintptr_t>(p) % 16;
+    if (!first && off != at) return kRowsAny;
+    at = off;
+    first = false;
+  }
+  return at == 0 && pitch % 16 == 0 && aligned16(codes) ? kRowsAligned : kRowsShifted;
+}
 
 // Run `launch(ws)` with the caller's workspace, or with one taken
 // stream-ordered from the library's pool when `own` is set.
@@ -112,9 +129,8 @@ fk_status rmsnorm_bwd_call(const void* dy, const void* h, const float* gamma, co
     if (overlap(sp[5], sp[i])) return FK_ERR_INVALID_ARG;
   st = check_memory(sp, 6);
   if (st != FK_OK) return st;
-  RmsnormBwdArgs a = {dy, h, gamma, dres, dx, dgamma, rows, cols, dtype, eps, false};
-  a.aligned = aligned16(dy) && aligned16(h) && aligned16(gamma) && aligned16(dres) && aligned16(dx) &&
-              (cols * es) % 16 == 0;
+  const RmsnormBwdArgs a = {dy, h, gamma, dres, dx, dgamma, rows, cols, dtype, eps,
+                            row_mode(cols * es, {dy, h, dres, dx}, gamma, nullptr)};
   const size_t need = rmsnorm_bwd_workspace(rows, cols, dtype, dgamma != nullptr);
   return with_workspace(need, ws, ws_bytes, own, sp, 6, s,
                         [&](void* w) { return launch_rmsnorm_bwd(a, w, s); });
@@ -178,9 +194,8 @@ fk_status fk_rmsnorm_rows(const void* x, const void* residual, const float* gamm
   if (overlap(sy, ss) || overlap(sy, sh) || overlap(ss, sh)) return FK_ERR_INVALID_ARG;
   st = check_memory(sp, 6);
   if (st != FK_OK) return st;
-  RmsnormArgs a = {x, residual, gamma, y, scales, h, rows, cols, dtype, out_dtype, eps, false};
-  a.aligned = aligned16(x) && aligned16(residual) && aligned16(gamma) && aligned16(y) && aligned16(h) &&
-              (cols * es) % 16 == 0;
+  const RowMode mode = row_mode(cols * es, {x, residual, h, q8 ? nullptr : y}, gamma, q8 ? y : nullptr);
+  const RmsnormArgs a = {x, residual, gamma, y, scales, h, rows, cols, dtype, out_dtype, eps, mode};
   return report_cuda(launch_rmsnorm(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -221,8 +236,7 @@ fk_status fk_quantize_rows(const void* x, void* q, float* scales, size_t rows, s
   if (overlap(sp[0], sp[1]) || overlap(sp[0], sp[2]) || overlap(sp[1], sp[2])) return FK_ERR_INVALID_ARG;
   st = check_memory(sp, 3);
   if (st != FK_OK) return st;
-  const bool aligned = aligned16(x) && aligned16(q) && (cols * es) % 16 == 0;
-  const QuantizeArgs a = {x, q, scales, rows, cols, dtype, out_dtype, epilogue, aligned};
+  const QuantizeArgs a = {x, q, scales, rows, cols, dtype, out_dtype, epilogue, row_mode(cols * es, {x}, nullptr, q)};
   return report_cuda(launch_quantize(a, static_cast<cudaStream_t>(stream)));
 }
 

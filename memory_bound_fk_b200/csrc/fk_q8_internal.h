@@ -43,9 +43,12 @@ cudaError_t launch_overlapped(void (*kernel)(KArgs...), unsigned grid, unsigned 
 }
 
 // ---- RMSNorm ---------------------------------------------------------------
-// Validated arguments of fk_rmsnorm_rows.  `aligned`: every row of x,
-// residual, h and y (and gamma) allows 16-byte vector access (8- or 4-byte
-// stores for 8-bit y).
+// How rows lie in memory: every row on a 16-byte boundary; rows shifted
+// against such boundaries, but alike in every buffer of their type; or
+// anything else (streamed one value at a time).
+enum RowMode { kRowsAligned, kRowsShifted, kRowsAny };
+
+// Validated arguments of fk_rmsnorm_rows.
 struct RmsnormArgs {
   const void* x;
   const void* residual;  // or nullptr
@@ -56,7 +59,7 @@ struct RmsnormArgs {
   size_t rows, cols;
   int dtype, out_dtype;
   float eps;
-  bool aligned;
+  RowMode mode;
 };
 cudaError_t launch_rmsnorm(const RmsnormArgs& a, cudaStream_t stream);
 
@@ -70,7 +73,7 @@ struct RmsnormBwdArgs {
   size_t rows, cols;
   int dtype;
   float eps;
-  bool aligned;
+  RowMode mode;
 };
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma);
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, void* ws, cudaStream_t stream);
@@ -82,7 +85,7 @@ struct QuantizeArgs {
   float* scales;
   size_t rows, cols;
   int dtype, out_dtype, epilogue;
-  bool aligned;
+  RowMode mode;
 };
 cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream);
 

@@ -3,9 +3,15 @@
 // warps as the row needs) reads a row once, keeps its values in registers as
 // fp32, reduces them once, and writes the outputs.
 //
-// Placement: with 16-byte vectors (aligned rows) thread t of the team holds
-// vectors t, team + t, 2 team + t, ...; otherwise values t, team + t, ...,
-// one at a time.  Either way a warp's accesses are contiguous.
+// Placement: 16-byte vectors of VEC values; thread t of the team holds vectors
+// t, team + t, 2 team + t, ..., so a warp's accesses are contiguous.  Rows
+// whose pitch is not a multiple of 16 bytes (ALIGNED = false) start `lead`
+// values past a 16-byte boundary, another lead for every row: there vector 0
+// is the one that holds the boundary, the first and the last vector of a row
+// are accessed value by value (only what belongs to the row), and parameters
+// and codes are shifted in registers.  Inputs and outputs of the rows' type
+// then have to sit alike to 16 bytes; other buffers are streamed.  4099 rows
+// of 1001 fp32: XXX us against YYY one value at a time.
 //
 // Bound by HBM.  A thread holds 16 values (rows up to 4096 columns) or 32:
 // the loads of both inputs are all in flight before the first is used.
@@ -30,17 +36,52 @@ constexpr int kRowWarpCols = 1024;     // rows up to here take one warp
 constexpr int kRowSmallCols = 4096;    // up to here 16 values a thread
 constexpr int kRowLargeCols = 16384;   // up to here 32 values a thread, at most 512 threads
 constexpr int kRowMaxCols = 32768;     // the same, at most 1024 threads; longer rows are streamed
+// Columns a shifted row may take besides its own: up to VEC - 1 before it.
+constexpr size_t row_span(size_t cols, bool aligned, int vec) { return aligned ? cols : cols + vec - 1; }
 constexpr size_t kRowMaxGrid = 0x7fffffffu;
 
-// A thread's place in its team.
+// A thread's place in its team, and the row's offset from a 16-byte boundary
+// in values (0 when ALIGNED).
 struct Place {
-  int t, team, cols;
+  int t, team, cols, lead;
 };
 
-// Is value k of chunk c one of the row's, and which.
-template <int VEC, bool ALIGNED>
+// Column of value k of chunk c (outside [0, cols): not one of the row's).
+template <int VEC>
 __device__ __forceinline__ int col_at(const Place& p, int c, int k) {
-  return ALIGNED ? (c * p.team + p.t) * VEC + k : (c * VEC + k) * p.team + p.t;
+  return (c * p.team + p.t) * VEC + k - p.lead;
+}
+
+// Values between `p` and the 16-byte boundary before it.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+}
+
+// The vector at column e of a row where it crosses the row's ends: its values
+// one at a time.  Out of line: one or two threads of a row come here.
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T* row, int e, int cols) {
+  constexpr int VEC = Elem<T>::VEC;
+  float f[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) f[k] = e + k >= 0 && e + k < cols ? static_cast<float>(row[e + k]) : 0.0f;
+  return Elem<T>::pack(f);  // exact
+}
+template <typename T>
+__device__ __noinline__ void store_edge(T* row, int e, int cols, uint4 w) {
+  constexpr int VEC = Elem<T>::VEC;
+  float f[VEC];
+  Elem<T>::unpack(w, f);
+#pragma unroll
+  for (int k = 0; k < VEC; ++k)
+    if (e + k >= 0 && e + k < cols) Elem<T>::store1(row + e + k, f[k]);  // exact
+}
+// Bytes first .. 3 of a word of codes whose first byte is column e.
+__device__ __noinline__ void store_code_edge(uint8_t* row, int e, int cols, int first, uint32_t w) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b >= first && e + b >= 0 && e + b < cols) row[e + b] = static_cast<uint8_t>(w >> (8 * b));
 }
 
 // The thread's VPT chunks of a row, as packed 16-byte words; zeros outside.
@@ -49,17 +90,12 @@ __device__ __forceinline__ void load_place(const T* row, const Place& p, uint4* 
   constexpr int VEC = Elem<T>::VEC;
 #pragma unroll
   for (int c = 0; c < VPT; ++c) {
+    const int e = col_at<VEC>(p, c, 0);
     if constexpr (ALIGNED) {
-      const int e = col_at<VEC, true>(p, c, 0);
       raw[c] = ld_stream_v4_if(row + e, e < p.cols, 0u);
     } else {
-      float f[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int e = col_at<VEC, false>(p, c, k);
-        f[k] = e < p.cols ? Elem<T>::load1(row + e) : 0.0f;
-      }
-      raw[c] = Elem<T>::pack(f);  // exact
+      raw[c] = ld_stream_v4_if(row + e, e >= 0 && e + VEC <= p.cols, 0u);
+      if ((e < 0 || e + VEC > p.cols) && e + VEC > 0 && e < p.cols) raw[c] = load_edge(row, e, p.cols);
     }
   }
 }
@@ -68,53 +104,64 @@ __device__ __forceinline__ void load_place(const T* row, const Place& p, uint4* 
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_place(T* row, const Place& p, int c, uint4 w) {
   constexpr int VEC = Elem<T>::VEC;
+  const int e = col_at<VEC>(p, c, 0);
   if constexpr (ALIGNED) {
-    const int e = col_at<VEC, true>(p, c, 0);
     if (e < p.cols) *reinterpret_cast<uint4*>(row + e) = w;
   } else {
-    float f[VEC];
-    Elem<T>::unpack(w, f);
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const int e = col_at<VEC, false>(p, c, k);
-      if (e < p.cols) Elem<T>::store1(row + e, f[k]);  // exact
-    }
+    if (e >= 0 && e + VEC <= p.cols)
+      *reinterpret_cast<uint4*>(row + e) = w;
+    else if (e + VEC > 0 && e < p.cols)
+      store_edge(row, e, p.cols, w);
   }
 }
 
-// One chunk stored as codes (zeros for a row that is not finite).
+// One chunk stored as codes (zeros for a row that is not finite).  Every lane
+// of the warp takes part.  Shifted rows: a lane's codes start s bytes past a
+// 4-byte boundary, the same s for the whole row; each lane writes the aligned
+// words that end in its own codes, the first of them completed by the last
+// codes of the lane before it.
 template <typename T, int OUT, bool ALIGNED>
 __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, int c, const float* v, const RowScale& q) {
-  constexpr int VEC = Elem<T>::VEC;
-  if constexpr (ALIGNED) {
-    const int e = col_at<VEC, true>(p, c, 0);
-    uint32_t w[VEC / 4];
+  constexpr int VEC = Elem<T>::VEC, W = VEC / 4;
+  const int e = col_at<VEC>(p, c, 0);
+  uint32_t w[W];
 #pragma unroll
-    for (int k = 0; k < VEC / 4; ++k) w[k] = q.ok ? Code8<OUT>::pack4(v + 4 * k, q.inv) : 0u;
+  for (int k = 0; k < W; ++k) w[k] = q.ok ? Code8<OUT>::pack4(v + 4 * k, q.inv) : 0u;
+  if constexpr (ALIGNED) {
     if (e < p.cols) {
-      if constexpr (VEC == 8)
+      if constexpr (W == 2)
         *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
       else
         *reinterpret_cast<uint32_t*>(row + e) = w[0];
     }
   } else {
+    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row + e) & 3), lane = threadIdx.x & 31;
+    uint32_t before = __shfl_up_sync(0xffffffffu, w[W - 1], 1);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const int e = col_at<VEC, false>(p, c, k);
-      if (e < p.cols) row[e] = q.ok ? Code8<OUT>::pack1(v[k], q.inv) : 0;
+    for (int k = 0; k < W; ++k) {
+      const uint32_t word = __funnelshift_l(before, w[k], 8 * s);
+      const int at = e - s + 4 * k;                     // column of the word's first byte
+      const int first = k == 0 && lane == 0 ? s : 0;    // the warp before wrote those
+      if (first == 0 && at >= 0 && at + 4 <= p.cols)
+        *reinterpret_cast<uint32_t*>(row + at) = word;
+      else if (at + 4 > 0 && at < p.cols)
+        store_code_edge(row, at, p.cols, first, word);
+      before = w[k];
     }
+    if (lane == 31 && s != 0 && e + VEC - s < p.cols && e + VEC > 0)
+      store_code_edge(row, e + VEC - s, p.cols < e + VEC ? p.cols : e + VEC, 0, w[W - 1] >> (8 * (4 - s)));
   }
 }
 
-// VEC fp32 parameters of chunk c (nullptr: ones).  The same for every row,
-// so they come from L1 and L2.
+// VEC fp32 parameters of chunk c (nullptr: ones), 16-byte aligned at column
+// 0.  The same for every row, so they come from L1 and L2.
 template <int VEC, bool ALIGNED>
 __device__ __forceinline__ void load_params(const float* g, const Place& p, int c, float* out) {
+  const int e = col_at<VEC>(p, c, 0);
 #pragma unroll
   for (int k = 0; k < VEC; ++k) out[k] = 1.0f;
   if (g == nullptr) return;
   if constexpr (ALIGNED) {
-    const int e = col_at<VEC, true>(p, c, 0);
     if (e < p.cols) {
 #pragma unroll
       for (int k = 0; k < VEC; k += 4) {
@@ -126,11 +173,31 @@ __device__ __forceinline__ void load_params(const float* g, const Place& p, int 
       }
     }
   } else {
+    // the aligned groups of four around e, then a shift by r = e mod 4 (the
+    // same for the whole row)
+    const int r = e & 3, from = e - r;
+    float a[VEC + 4];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const int e = col_at<VEC, false>(p, c, k);
-      if (e < p.cols) out[k] = __ldg(g + e);
+    for (int k = 0; k < VEC + 4; k += 4) {
+      float4 z = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+      const int i = from + k;
+      if (i >= 0 && i + 4 <= p.cols) {
+        z = __ldg(reinterpret_cast<const float4*>(g + i));
+      } else if (i + 4 > 0 && i < p.cols) {
+        if (i >= 0) z.x = __ldg(g + i);
+        if (i + 1 >= 0 && i + 1 < p.cols) z.y = __ldg(g + i + 1);
+        if (i + 2 >= 0 && i + 2 < p.cols) z.z = __ldg(g + i + 2);
+        if (i + 3 < p.cols) z.w = __ldg(g + i + 3);
+      }
+      a[k] = z.x;
+      a[k + 1] = z.y;
+      a[k + 2] = z.z;
+      a[k + 3] = z.w;
     }
+#pragma unroll
+    for (int k = 0; k < VEC + 2; ++k) a[k] = (r & 1) ? a[k + 1] : a[k];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) out[k] = (r & 2) ? a[k + 2] : a[k];
   }
 }
 
@@ -158,10 +225,10 @@ template <bool WARP, typename F>
 __device__ __forceinline__ void for_rows(size_t rows, int cols, F fn) {
   if constexpr (WARP) {
     const size_t per = blockDim.x >> 5, stride = gridDim.x * per;
-    const Place p = {static_cast<int>(threadIdx.x & 31), 32, cols};
+    const Place p = {static_cast<int>(threadIdx.x & 31), 32, cols, 0};
     for (size_t row = blockIdx.x * per + (threadIdx.x >> 5); row < rows; row += stride) fn(row, p);
   } else {
-    const Place p = {static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), cols};
+    const Place p = {static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), cols, 0};
     for (size_t row = blockIdx.x; row < rows; row += gridDim.x) {
       fn(row, p);
       if (row + gridDim.x < rows) __syncthreads();  // the reduction's scratch is used again
@@ -183,9 +250,10 @@ inline RowLaunch warp_launch(size_t rows) {
   return {static_cast<unsigned>(blocks < kRowMaxGrid ? blocks : kRowMaxGrid), static_cast<unsigned>(32 * per)};
 }
 
-// One block per row, as many warps as hold it at ept values a thread.
-inline RowLaunch block_launch(size_t rows, size_t cols, int ept) {
-  const size_t threads = ((cols + ept - 1) / ept + 31) / 32 * 32;
+// One block per row, as many warps as hold it at ept values a thread (`span`:
+// the columns, and the lead where rows are shifted).
+inline RowLaunch block_launch(size_t rows, size_t span, int ept) {
+  const size_t threads = ((span + ept - 1) / ept + 31) / 32 * 32;
   return {static_cast<unsigned>(rows < kRowMaxGrid ? rows : kRowMaxGrid), static_cast<unsigned>(threads)};
 }
 

@@ -37,8 +37,9 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(QuantizeArgs a
   __shared__ float2 red[WARP ? 1 : MAXT / 32];
   let_next_start();
   after_previous();
-  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, const Place& p) {
+  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, Place p) {
     const size_t base = row * a.cols;
+    if (!ALIGNED) p.lead = lead_of(static_cast<const T*>(a.x) + base);
     uint4 raw[VPT];
     load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.x) + base, p, raw);
     float v[EPT], s = 0.0f, m = 0.0f;
@@ -88,33 +89,34 @@ __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(Quantiz
 
 template <typename T, int OUT, int EPI, bool ALIGNED>
 cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
-  if (a.cols <= kRowWarpCols) {
+  const size_t span = row_span(a.cols, ALIGNED, Elem<T>::VEC);
+  if (span <= kRowWarpCols) {
     const RowLaunch l = warp_launch(a.rows);
-    if (a.cols <= kRowWarpCols / 4)
+    if (span <= kRowWarpCols / 4)
       return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 8, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-    else if (a.cols <= kRowWarpCols / 2)
+    else if (span <= kRowWarpCols / 2)
       return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
     else
       return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-  } else if (a.cols <= kRowSmallCols) {
-    const RowLaunch l = block_launch(a.rows, a.cols, 16);
+  } else if (span <= kRowSmallCols) {
+    const RowLaunch l = block_launch(a.rows, span, 16);
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  } else if (a.cols <= kRowLargeCols) {
-    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+  } else if (span <= kRowLargeCols) {
+    const RowLaunch l = block_launch(a.rows, span, 32);
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else {
-    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+    const RowLaunch l = block_launch(a.rows, span, 32);
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
   }
 }
 
 template <typename T, int OUT, int EPI>
 cudaError_t launch_epi(const QuantizeArgs& a, cudaStream_t s) {
-  if (a.cols > kRowMaxCols) {
+  if (row_span(a.cols, a.mode == kRowsAligned, Elem<T>::VEC) > kRowMaxCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     return launch_overlapped(quantize_stream_kernel<T, OUT, EPI>, g, kStreamThreads, 0, 1, s, a);
   }
-  return a.aligned ? launch_rows<T, OUT, EPI, true>(a, s) : launch_rows<T, OUT, EPI, false>(a, s);
+  return a.mode == kRowsAligned ? launch_rows<T, OUT, EPI, true>(a, s) : launch_rows<T, OUT, EPI, false>(a, s);
 }
 
 template <typename T, int OUT>

@@ -37,8 +37,9 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(RmsnormArgs a) 
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   let_next_start();
   after_previous();
-  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, const Place& p) {
+  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, Place p) {
     const size_t base = row * a.cols;
+    if (!ALIGNED) p.lead = lead_of(static_cast<const T*>(a.x) + base);
     uint4 raw[VPT];
     load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.x) + base, p, raw);
     if (a.residual) {
@@ -143,33 +144,34 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
 
 template <typename T, int OUT, bool ALIGNED>
 cudaError_t launch_rows(const RmsnormArgs& a, cudaStream_t s) {
-  if (a.cols <= kRowWarpCols) {
+  const size_t span = row_span(a.cols, ALIGNED, Elem<T>::VEC);
+  if (span <= kRowWarpCols) {
     const RowLaunch l = warp_launch(a.rows);
-    if (a.cols <= kRowWarpCols / 4)
+    if (span <= kRowWarpCols / 4)
       return launch_overlapped(rmsnorm_row_kernel<T, OUT, 8, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-    else if (a.cols <= kRowWarpCols / 2)
+    else if (span <= kRowWarpCols / 2)
       return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
     else
       return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-  } else if (a.cols <= kRowSmallCols) {
-    const RowLaunch l = block_launch(a.rows, a.cols, 16);
+  } else if (span <= kRowSmallCols) {
+    const RowLaunch l = block_launch(a.rows, span, 16);
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  } else if (a.cols <= kRowLargeCols) {
-    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+  } else if (span <= kRowLargeCols) {
+    const RowLaunch l = block_launch(a.rows, span, 32);
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else {
-    const RowLaunch l = block_launch(a.rows, a.cols, 32);
+    const RowLaunch l = block_launch(a.rows, span, 32);
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
   }
 }
 
 template <typename T, int OUT>
 cudaError_t launch_out(const RmsnormArgs& a, cudaStream_t s) {
-  if (a.cols > kRowMaxCols) {
+  if (a.mode == kRowsAny || row_span(a.cols, a.mode == kRowsAligned, Elem<T>::VEC) > kRowMaxCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     return launch_overlapped(rmsnorm_stream_kernel<T, OUT>, g, kStreamThreads, 0, 1, s, a);
   }
-  return a.aligned ? launch_rows<T, OUT, true>(a, s) : launch_rows<T, OUT, false>(a, s);
+  return a.mode == kRowsAligned ? launch_rows<T, OUT, true>(a, s) : launch_rows<T, OUT, false>(a, s);
 }
 
 template <typename T>

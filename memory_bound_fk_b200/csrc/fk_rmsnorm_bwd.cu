@@ -55,12 +55,14 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs
   const float inv_n = 1.0f / static_cast<float>(cols);
   const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const Place p = WARP ? Place{static_cast<int>(threadIdx.x & 31), 32, cols}
-                       : Place{static_cast<int>(rank * blockDim.x + threadIdx.x), static_cast<int>(TEAMS * blockDim.x), cols};
+  Place p = WARP ? Place{static_cast<int>(threadIdx.x & 31), 32, cols, 0}
+                 : Place{static_cast<int>(rank * blockDim.x + threadIdx.x), static_cast<int>(TEAMS * blockDim.x), cols, 0};
   const size_t team = WARP ? static_cast<size_t>(blockIdx.x) * warps + warp : blockIdx.x / TEAMS;
   const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps : gridDim.x / TEAMS;
   const T* const h = static_cast<const T*>(a.h);
   const T* const dy = static_cast<const T*>(a.dy);
+  // a team's rows are a multiple of eight apart (or it has one): their lead is the same
+  if (!ALIGNED) p.lead = lead_of(h + team * a.cols);
   let_next_start();
   after_previous();
   if constexpr (CL > 1) cluster_arrive_relaxed();  // every block has started: waited for before the first push
@@ -155,8 +157,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs
     for (int c = 0; c < VPT; ++c)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const int e = col_at<VEC, ALIGNED>(p, c, k);
-        if (e < cols) sums[warp][e] = acc[c * VEC + k];
+        const int e = col_at<VEC>(p, c, k);
+        if (e >= 0 && e < cols) sums[warp][e] = acc[c * VEC + k];
       }
     __syncthreads();
     for (int e = threadIdx.x; e < cols; e += blockDim.x) {
@@ -169,8 +171,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs
     for (int c = 0; c < VPT; ++c)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const int e = col_at<VEC, ALIGNED>(p, c, k);
-        if (e < cols) out[e] = acc[c * VEC + k];
+        const int e = col_at<VEC>(p, c, k);
+        if (e >= 0 && e < cols) out[e] = acc[c * VEC + k];
       }
   }
 }
@@ -306,11 +308,13 @@ struct BwdLaunch {
 };
 
 // Teams stay resident: as many blocks as fit the registers (128 a thread).
-BwdLaunch bwd_launch(size_t rows, size_t cols) {
+// `span`: the columns, and the lead where rows are shifted; their teams then
+// walk rows a multiple of eight apart.
+BwdLaunch bwd_launch(size_t rows, size_t span, bool shifted) {
   BwdLaunch l;
-  if (cols <= static_cast<size_t>(kRowWarpCols)) {
+  if (span <= static_cast<size_t>(kRowWarpCols)) {
     // a warp per row, 8 / 16 / 32 values a lane (about 80 / 110 / 200 registers: 3 / 2 / 1 blocks per SM)
-    l.ept = cols <= 256 ? 8 : cols <= 512 ? 16 : 32;
+    l.ept = span <= 256 ? 8 : span <= 512 ? 16 : 32;
     l.cluster = 0;
     l.threads = 32 * kRowWarps;
     const size_t fit = kSmCount * (l.ept == 8 ? 3 : l.ept == 16 ? 2 : 1), want = (rows + kRowWarps - 1) / kRowWarps;
@@ -318,11 +322,11 @@ BwdLaunch bwd_launch(size_t rows, size_t cols) {
     return l;
   }
   l.ept = kBwdEpt;
-  l.cluster = cols <= kBwdBlockCols ? 1 : cols <= 2 * kBwdBlockCols ? 2 : 4;
+  l.cluster = span <= kBwdBlockCols ? 1 : span <= 2 * kBwdBlockCols ? 2 : 4;
   const size_t per = kBwdEpt * static_cast<size_t>(l.cluster);
-  l.threads = static_cast<int>(((cols + per - 1) / per + 31) / 32 * 32);
+  l.threads = static_cast<int>(((span + per - 1) / per + 31) / 32 * 32);
   const size_t fit = kSmCount / l.cluster * (l.cluster == 1 ? kBwdThreads / l.threads : 1);
-  l.groups = rows < fit ? rows : fit;
+  l.groups = rows < fit ? rows : shifted ? fit / 8 * 8 : fit;
   l.blocks = l.groups * l.cluster;
   return l;
 }
@@ -336,7 +340,7 @@ cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const Bwd
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
-  const BwdLaunch l = bwd_launch(a.rows, a.cols);
+  const BwdLaunch l = bwd_launch(a.rows, row_span(a.cols, ALIGNED, Elem<T>::VEC), !ALIGNED);
   float* partial = a.dgamma ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaErrorInvalidValue;
   if (l.cluster == 0) {
@@ -354,16 +358,24 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
-  if (a.cols > 4 * kBwdBlockCols) return launch_stream<T>(a, ws, s);
-  return a.aligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
+  // rows too long for a cluster's registers, or buffers that lie differently
+  if (a.mode == kRowsAny || row_span(a.cols, a.mode == kRowsAligned, Elem<T>::VEC) > 4 * kBwdBlockCols)
+    return launch_stream<T>(a, ws, s);
+  return a.mode == kRowsAligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
 }
 
 }  // namespace
 
+// Enough for every way the buffers may lie.
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
-  (void)dtype;
-  if (cols > 4 * kBwdBlockCols) return stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
-  return want_dgamma ? bwd_launch(rows, cols).groups * cols * sizeof(float) : 0;
+  const size_t stream = stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
+  if (cols > 4 * kBwdBlockCols || !want_dgamma) return stream;
+  const size_t span = row_span(cols, false, vec_elems(dtype));
+  size_t groups = bwd_launch(rows, cols, false).groups;
+  const size_t shifted = bwd_launch(rows, span, true).groups;
+  if (shifted > groups) groups = shifted;
+  const size_t rowed = groups * cols * sizeof(float);
+  return rowed > stream ? rowed : stream;
 }
 
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, void* ws, cudaStream_t stream) {

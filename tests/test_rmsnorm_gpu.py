@@ -97,8 +97,25 @@ def test_many_rows(fk, torch_mod, rows, cols, dtype, out):
 @pytest.mark.parametrize("cols", [64, 1000, 4096, 40000])
 def test_misaligned_buffers(fk, torch_mod, cols, dtype, out):
     x, r, g = make_rows(4, cols, dtype, 1), make_rows(4, cols, dtype, 2), gamma_of(cols, 3)
-    for off in ((1, 0, 0, 0, 0), (0, 1, 0, 0, 0), (0, 0, 1, 0, 0), (0, 0, 0, 1, 0), (0, 0, 0, 0, 1), (1, 3, 5, 2, 1)):
+    for off in ((1, 0, 0, 0, 0), (0, 1, 0, 0, 0), (0, 0, 1, 0, 0), (0, 0, 0, 1, 0), (0, 0, 0, 0, 1), (1, 3, 5, 2, 1), (1, 1, 1, 1, 0), (3, 3, 3, 3, 0),
+                (2, 2, 7, 2, 0)):
         check_forward(x, r, g, out, forward(fk, torch_mod, x, r, g, out, off=off))
+
+
+@pytest.mark.parametrize("out", [None, "i8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1, 2, 3, 5, 8, 9, 15, 31, 33, 250, 255, 257, 505, 513, 1017, 1021, 1025, 2047, 4089, 4091,
+                                  4093, 4097, 8191, 16379, 32761, 32765])
+def test_rows_that_start_off_16_bytes(fk, torch_mod, cols, dtype, out):
+    """Every lead a row can have (nine rows of an odd width), around the widths where the kernels change."""
+    x, r, g = make_rows(9, cols, dtype, cols), make_rows(9, cols, dtype, cols + 1), gamma_of(cols, 3)
+    check_forward(x, r, g, out, forward(fk, torch_mod, x, r, g, out))
+    check_forward(x, r, g, out, forward(fk, torch_mod, x, r, g, out, off=(1, 1, 1, 1, 0)))
+    if out is None:
+        check_forward(x, r, g, out, forward(fk, torch_mod, x, r, g, out, alias="h=r"))
+        dy = make_rows(9, cols, dtype, cols + 2)
+        check_backward(dy, x, g, r, backward(fk, torch_mod, dy, x, g, r))
+        check_backward(dy, x, g, r, backward(fk, torch_mod, dy, x, g, r, off=0, alias="dy"))
 
 
 @pytest.mark.parametrize("alias", ["h=x", "h=r", "y=x", "y=r"])
@@ -198,7 +215,8 @@ def check_backward(dy, h, gamma, dres, got, eps=1e-6):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,cols", SHAPES + [(300, 64), (1200, 1000), (999, 4096), (150, 8192), (130, 16384)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(300, 64), (1200, 1000), (999, 4096), (150, 8192), (130, 16384), (999, 2047), (3001, 255),
+                                                (1300, 511), (1201, 1001), (170, 8193), (90, 20001)])
 def test_backward(fk, torch_mod, rows, cols, dtype):
     dy, h, dr = (make_rows(rows, cols, dtype, cols + i, 0.3) for i in range(3))
     g = gamma_of(cols, cols)
