@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kRowWarps = 8;           // rows (warps) per block on the warp path, at most
 constexpr int kRowWarpCols = 1024;     // rows up to here take one warp
-constexpr int kRowSmallCols = 4096;    // up to here 16 values a thread
+constexpr int kRowSmallCols = 8192;    // up to here four vectors a thread
 constexpr int kRowLargeCols = 16384;   // up to here 32 values a thread, at most 512 threads
 constexpr int kRowMaxCols = 32768;     // the same, at most 1024 threads; longer rows are streamed
 // Columns a shifted row may take besides its own: up to VEC - 1 before it.
@@ -58,46 +58,82 @@ __device__ __forceinline__ int lead_of(const T* p) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
 }
 
-// The vector at column e of a row where it crosses the row's ends: its values
-// one at a time.  Out of line: one or two threads of a row come here.
+// The rows of one buffer: where the row at hand starts, and the buffer's ends.
 template <typename T>
-__device__ __noinline__ uint4 load_edge(const T* row, int e, int cols) {
-  constexpr int VEC = Elem<T>::VEC;
-  float f[VEC];
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) f[k] = e + k >= 0 && e + k < cols ? static_cast<float>(row[e + k]) : 0.0f;
-  return Elem<T>::pack(f);  // exact
+struct RowOf {
+  T* row;
+  const T* begin;
+  const T* end;
+};
+template <typename T>
+__device__ __forceinline__ RowOf<T> row_of(T* buffer, size_t first, size_t count) {
+  return RowOf<T>{buffer + first, buffer, buffer + count};
 }
+
+// Values outside columns [0, cols) of the vector at column e set to zero.
 template <typename T>
-__device__ __noinline__ void store_edge(T* row, int e, int cols, uint4 w) {
+__device__ __forceinline__ uint4 mask_edge(uint4 w, int e, int cols) {
   constexpr int VEC = Elem<T>::VEC;
   float f[VEC];
   Elem<T>::unpack(w, f);
 #pragma unroll
-  for (int k = 0; k < VEC; ++k)
-    if (e + k >= 0 && e + k < cols) Elem<T>::store1(row + e + k, f[k]);  // exact
-}
-// Bytes first .. 3 of a word of codes whose first byte is column e.
-__device__ __noinline__ void store_code_edge(uint8_t* row, int e, int cols, int first, uint32_t w) {
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-    if (b >= first && e + b >= 0 && e + b < cols) row[e + b] = static_cast<uint8_t>(w >> (8 * b));
+  for (int k = 0; k < VEC; ++k) f[k] = e + k >= 0 && e + k < cols ? f[k] : 0.0f;
+  return Elem<T>::pack(f);  // exact
 }
 
 // The thread's VPT chunks of a row, as packed 16-byte words; zeros outside.
+// Shifted rows: a vector that crosses a row's end is loaded whole (its other
+// values belong to the neighbouring rows; mask_place() takes them out once
+// the loads are used, so that nothing waits here); only where that would
+// leave the buffer, at its first and last vector, are values loaded one at a
+// time.
 template <typename T, int VPT, bool ALIGNED>
-__device__ __forceinline__ void load_place(const T* row, const Place& p, uint4* raw) {
+__device__ __forceinline__ void load_place(const RowOf<const T>& r, const Place& p, uint4* raw) {
   constexpr int VEC = Elem<T>::VEC;
 #pragma unroll
   for (int c = 0; c < VPT; ++c) {
     const int e = col_at<VEC>(p, c, 0);
+    const T* const at = r.row + e;
     if constexpr (ALIGNED) {
-      raw[c] = ld_stream_v4_if(row + e, e < p.cols, 0u);
+      raw[c] = ld_stream_v4_if(at, e < p.cols, 0u);
     } else {
-      raw[c] = ld_stream_v4_if(row + e, e >= 0 && e + VEC <= p.cols, 0u);
-      if ((e < 0 || e + VEC > p.cols) && e + VEC > 0 && e < p.cols) raw[c] = load_edge(row, e, p.cols);
+      const bool any = e + VEC > 0 && e < p.cols, inside = at >= r.begin && at + VEC <= r.end;
+      raw[c] = ld_stream_v4_if(at, any && inside, 0u);
+      if (any && !inside) {
+        float f[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          f[k] = e + k >= 0 && e + k < p.cols ? static_cast<float>(at[k]) : 0.0f;
+        raw[c] = Elem<T>::pack(f);  // exact
+      }
     }
   }
+}
+
+// Zeros in place of what a shifted row's first and last vector hold of other
+// rows.
+template <typename T, int VPT, bool ALIGNED>
+__device__ __forceinline__ void mask_place(const Place& p, uint4* raw) {
+  if constexpr (!ALIGNED) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      const int e = col_at<Elem<T>::VEC>(p, c, 0);
+      if (e < 0 || e + Elem<T>::VEC > p.cols) raw[c] = mask_edge<T>(raw[c], e, p.cols);
+    }
+  }
+}
+
+// Stores that stay where they are written in program order: left to itself
+// the compiler gathers a row's stores at its end, and 16384 x 4096 bf16 (x +
+// residual in, h and y out) goes from 94 us to 107.
+__device__ __forceinline__ void st_v4(void* p, uint4 v) {
+  asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_v2(void* p, uint32_t x, uint32_t y) {
+  asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void st_v1(void* p, uint32_t x) {
+  asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
 }
 
 // One chunk stored in the rows' own type from its packed words.
@@ -106,13 +142,25 @@ __device__ __forceinline__ void store_place(T* row, const Place& p, int c, uint4
   constexpr int VEC = Elem<T>::VEC;
   const int e = col_at<VEC>(p, c, 0);
   if constexpr (ALIGNED) {
-    if (e < p.cols) *reinterpret_cast<uint4*>(row + e) = w;
+    if (e < p.cols) st_v4(row + e, w);
   } else {
-    if (e >= 0 && e + VEC <= p.cols)
-      *reinterpret_cast<uint4*>(row + e) = w;
-    else if (e + VEC > 0 && e < p.cols)
-      store_edge(row, e, p.cols, w);
+    if (e >= 0 && e + VEC <= p.cols) {
+      st_v4(row + e, w);
+    } else if (e + VEC > 0 && e < p.cols) {
+      float f[VEC];
+      Elem<T>::unpack(w, f);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k)
+        if (e + k >= 0 && e + k < p.cols) Elem<T>::store1(row + e + k, f[k]);  // exact
+    }
   }
+}
+
+// Bytes first .. 3 of a word of codes whose first byte is column e.
+__device__ __forceinline__ void store_code_edge(uint8_t* row, int e, int cols, int first, uint32_t w) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b >= first && e + b >= 0 && e + b < cols) row[e + b] = static_cast<uint8_t>(w >> (8 * b));
 }
 
 // One chunk stored as codes (zeros for a row that is not finite).  Every lane
@@ -130,9 +178,9 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, int c,
   if constexpr (ALIGNED) {
     if (e < p.cols) {
       if constexpr (W == 2)
-        *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
+        st_v2(row + e, w[0], w[1]);
       else
-        *reinterpret_cast<uint32_t*>(row + e) = w[0];
+        st_v1(row + e, w[0]);
     }
   } else {
     const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row + e) & 3), lane = threadIdx.x & 31;
@@ -143,7 +191,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, int c,
       const int at = e - s + 4 * k;                     // column of the word's first byte
       const int first = k == 0 && lane == 0 ? s : 0;    // the warp before wrote those
       if (first == 0 && at >= 0 && at + 4 <= p.cols)
-        *reinterpret_cast<uint32_t*>(row + at) = word;
+        st_v1(row + at, word);
       else if (at + 4 > 0 && at < p.cols)
         store_code_edge(row, at, p.cols, first, word);
       before = w[k];
@@ -180,14 +228,13 @@ __device__ __forceinline__ void load_params(const float* g, const Place& p, int 
 #pragma unroll
     for (int k = 0; k < VEC + 4; k += 4) {
       float4 z = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-      const int i = from + k;
+      const int i = from + k;  // a multiple of 4: a group before column 0 holds none of the row's
       if (i >= 0 && i + 4 <= p.cols) {
         z = __ldg(reinterpret_cast<const float4*>(g + i));
-      } else if (i + 4 > 0 && i < p.cols) {
-        if (i >= 0) z.x = __ldg(g + i);
-        if (i + 1 >= 0 && i + 1 < p.cols) z.y = __ldg(g + i + 1);
-        if (i + 2 >= 0 && i + 2 < p.cols) z.z = __ldg(g + i + 2);
-        if (i + 3 < p.cols) z.w = __ldg(g + i + 3);
+      } else if (i >= 0 && i < p.cols) {
+        z.x = __ldg(g + i);
+        if (i + 1 < p.cols) z.y = __ldg(g + i + 1);
+        if (i + 2 < p.cols) z.z = __ldg(g + i + 2);
       }
       a[k] = z.x;
       a[k + 1] = z.y;

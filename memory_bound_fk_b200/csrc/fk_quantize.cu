@@ -32,7 +32,7 @@ __device__ __forceinline__ float2 act2(float2 x) {
 }
 
 template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, bool WARP, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(QuantizeArgs a) {
+__global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_constant__ QuantizeArgs a) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   __shared__ float2 red[WARP ? 1 : MAXT / 32];
   let_next_start();
@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(QuantizeArgs a
     const size_t base = row * a.cols;
     if (!ALIGNED) p.lead = lead_of(static_cast<const T*>(a.x) + base);
     uint4 raw[VPT];
-    load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.x) + base, p, raw);
+    load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.x), base, a.rows * a.cols), p, raw);
+    mask_place<T, VPT, ALIGNED>(p, raw);
     float v[EPT], s = 0.0f, m = 0.0f;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -99,8 +100,9 @@ cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
     else
       return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   } else if (span <= kRowSmallCols) {
-    const RowLaunch l = block_launch(a.rows, span, 16);
-    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
+    constexpr int EPT = 4 * Elem<T>::VEC;
+    const RowLaunch l = block_launch(a.rows, span, EPT);
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, EPT, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else if (span <= kRowLargeCols) {
     const RowLaunch l = block_launch(a.rows, span, 32);
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);

@@ -30,7 +30,7 @@ __device__ __forceinline__ float round_to(float v) {
 // MAXT, MINB: threads and blocks per SM the registers are sized for (64 a
 // thread for 1024 threads on an SM).
 template <typename T, int OUT, int EPT, bool ALIGNED, bool WARP, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(RmsnormArgs a) {
+__global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_constant__ RmsnormArgs a) {
   constexpr bool Q8 = OUT == FK_I8 || OUT == FK_E4M3;
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   __shared__ float2 red[WARP ? 1 : MAXT / 32];
@@ -41,10 +41,10 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(RmsnormArgs a) 
     const size_t base = row * a.cols;
     if (!ALIGNED) p.lead = lead_of(static_cast<const T*>(a.x) + base);
     uint4 raw[VPT];
-    load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.x) + base, p, raw);
+    load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.x), base, a.rows * a.cols), p, raw);
     if (a.residual) {
       uint4 res[VPT];
-      load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.residual) + base, p, res);
+      load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.residual), base, a.rows * a.cols), p, res);
 #pragma unroll
       for (int c = 0; c < VPT; ++c) {
         float f[VEC], r[VEC];
@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(RmsnormArgs a) 
         if (a.h) store_place<T, ALIGNED>(static_cast<T*>(a.h) + base, p, c, raw[c]);
       }
     }
+    mask_place<T, VPT, ALIGNED>(p, raw);
     float v[EPT], s = 0.0f, m = 0.0f;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -154,8 +155,9 @@ cudaError_t launch_rows(const RmsnormArgs& a, cudaStream_t s) {
     else
       return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   } else if (span <= kRowSmallCols) {
-    const RowLaunch l = block_launch(a.rows, span, 16);
-    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
+    constexpr int EPT = 4 * Elem<T>::VEC;
+    const RowLaunch l = block_launch(a.rows, span, EPT);
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, EPT, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   } else if (span <= kRowLargeCols) {
     const RowLaunch l = block_launch(a.rows, span, 32);
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);

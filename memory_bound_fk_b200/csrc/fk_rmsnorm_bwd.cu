@@ -45,7 +45,7 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 // 16384 columns in one block: 3.4 TB/s at 32 values a thread, 3.0 with 1024
 // threads, hence the clusters.
 template <typename T, int EPT, bool ALIGNED, int CL, bool PF, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs a, float* partial) {
+__global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   constexpr bool WARP = CL == 0;
   constexpr int TEAMS = CL > 1 ? CL : 1;
@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs
   for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
   uint4 rh[VPT], rd[VPT];
   if (PF && team < a.rows) {
-    load_place<T, VPT, ALIGNED>(h + team * a.cols, p, rh);
-    load_place<T, VPT, ALIGNED>(dy + team * a.cols, p, rd);
+    load_place<T, VPT, ALIGNED>(row_of(h, team * a.cols, a.rows * a.cols), p, rh);
+    load_place<T, VPT, ALIGNED>(row_of(dy, team * a.cols, a.rows * a.cols), p, rd);
   }
   if constexpr (CL > 1) cluster_wait();
   int turn = 0;
@@ -82,14 +82,16 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(RmsnormBwdArgs
     const size_t base = row * a.cols;
     uint4 nh[VPT], nd[VPT], rr[VPT];
     if (!PF) {
-      load_place<T, VPT, ALIGNED>(h + base, p, rh);
-      load_place<T, VPT, ALIGNED>(dy + base, p, rd);
+      load_place<T, VPT, ALIGNED>(row_of(h, base, a.rows * a.cols), p, rh);
+      load_place<T, VPT, ALIGNED>(row_of(dy, base, a.rows * a.cols), p, rd);
     }
-    if (a.dres) load_place<T, VPT, ALIGNED>(static_cast<const T*>(a.dres) + base, p, rr);
+    if (a.dres) load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.dres), base, a.rows * a.cols), p, rr);
     if (PF && row + stride < a.rows) {
-      load_place<T, VPT, ALIGNED>(h + base + stride * a.cols, p, nh);
-      load_place<T, VPT, ALIGNED>(dy + base + stride * a.cols, p, nd);
+      load_place<T, VPT, ALIGNED>(row_of(h, base + stride * a.cols, a.rows * a.cols), p, nh);
+      load_place<T, VPT, ALIGNED>(row_of(dy, base + stride * a.cols, a.rows * a.cols), p, nd);
     }
+    mask_place<T, VPT, ALIGNED>(p, rh);
+    mask_place<T, VPT, ALIGNED>(p, rd);
     float s = 0.0f, d = 0.0f;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -333,7 +335,7 @@ BwdLaunch bwd_launch(size_t rows, size_t span, bool shifted) {
 
 template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
 cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, ALIGNED, MAXT>,
+  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, true, MAXT>,
                            static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), 0, CL > 1 ? CL : 1, s, a,
                            partial);
 }
