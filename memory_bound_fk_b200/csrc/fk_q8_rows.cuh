@@ -5,13 +5,11 @@
 //
 // Placement: 16-byte vectors of VEC values; thread t of the team holds vectors
 // t, team + t, 2 team + t, ..., so a warp's accesses are contiguous.  Rows
-// whose pitch is not a multiple of 16 bytes (ALIGNED = false) start `lead`
-// values past a 16-byte boundary, another lead for every row: there vector 0
-// is the one that holds the boundary, the first and the last vector of a row
-// are accessed value by value (only what belongs to the row), and parameters
-// and codes are shifted in registers.  Inputs and outputs of the rows' type
-// then have to sit alike to 16 bytes; other buffers are streamed.  4099 rows
-// of 1001 fp32: XXX us against YYY one value at a time.
+// whose pitch is not a multiple of 16 bytes (ALIGNED = false) start anywhere:
+// their vectors are those that lie on 16-byte boundaries inside the row, and
+// the at most 2 (VEC - 1) values before the first and behind the last belong
+// to the team's first threads, one each.  Inputs and outputs of the rows' type
+// then have to sit alike to 16 bytes; other buffers are streamed.
 //
 // Bound by HBM.  A thread holds 16 values (rows up to 4096 columns) or 32:
 // the loads of both inputs are all in flight before the first is used.
@@ -26,101 +24,68 @@
 
 #include "fk_common.cuh"
 #include "fk_q8.cuh"
-#include "fk_rows.cuh"
+#include "fk_sync.cuh"
 
 namespace fk {
 namespace {
 
-constexpr int kRowWarps = 8;           // rows (warps) per block on the warp path, at most
+constexpr int kRowWarps = 8;           // warps per block where a row takes a warp or less, at most
+constexpr int kRowLaneEpt = 8;         // values a thread where a row takes 8 or 16 lanes
 constexpr int kRowWarpCols = 1024;     // rows up to here take one warp
-constexpr int kRowSmallCols = 8192;    // up to here four vectors a thread
+constexpr int kRowBlockCols = 8192;    // up to here four vectors a thread
 constexpr int kRowLargeCols = 16384;   // up to here 32 values a thread, at most 512 threads
 constexpr int kRowMaxCols = 32768;     // the same, at most 1024 threads; longer rows are streamed
-// Columns a shifted row may take besides its own: up to VEC - 1 before it.
-constexpr size_t row_span(size_t cols, bool aligned, int vec) { return aligned ? cols : cols + vec - 1; }
 constexpr size_t kRowMaxGrid = 0x7fffffffu;
 
-// A thread's place in its team, and the row's offset from a 16-byte boundary
-// in values (0 when ALIGNED).
+// A thread's place in its team; the row's columns, how many of them come
+// before the first vector, and how many vectors there are.
 struct Place {
-  int t, team, cols, lead;
+  int t, team, cols, head, vecs;
 };
 
-// Column of value k of chunk c (outside [0, cols): not one of the row's).
+// Place of an aligned row (cols a multiple of VEC), or of the one at `row`.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ Place place_of(int t, int team, int cols, const T* row) {
+  constexpr int VEC = Elem<T>::VEC;
+  if constexpr (ALIGNED) return Place{t, team, cols, 0, cols / VEC};
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  int head = off == 0 ? 0 : VEC - off;
+  head = head < cols ? head : cols;
+  return Place{t, team, cols, head, (cols - head) / VEC};
+}
+
+// Is chunk c one of the row's vectors, and the column of its first value.
+__device__ __forceinline__ bool has_vec(const Place& p, int c) { return c * p.team + p.t < p.vecs; }
 template <int VEC>
-__device__ __forceinline__ int col_at(const Place& p, int c, int k) {
-  return (c * p.team + p.t) * VEC + k - p.lead;
+__device__ __forceinline__ int col_of_vec(const Place& p, int c) {
+  return p.head + (c * p.team + p.t) * VEC;
 }
 
-// Values between `p` and the 16-byte boundary before it.
-template <typename T>
-__device__ __forceinline__ int lead_of(const T* p) {
-  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+// The column outside the vectors that is this thread's, or -1.
+template <int VEC>
+__device__ __forceinline__ int edge_col(const Place& p) {
+  const int in = p.vecs * VEC;
+  return p.t < p.cols - in ? (p.t < p.head ? p.t : in + p.t) : -1;
 }
 
-// The rows of one buffer: where the row at hand starts, and the buffer's ends.
-template <typename T>
-struct RowOf {
-  T* row;
-  const T* begin;
-  const T* end;
-};
-template <typename T>
-__device__ __forceinline__ RowOf<T> row_of(T* buffer, size_t first, size_t count) {
-  return RowOf<T>{buffer + first, buffer, buffer + count};
-}
-
-// Values outside columns [0, cols) of the vector at column e set to zero.
-template <typename T>
-__device__ __forceinline__ uint4 mask_edge(uint4 w, int e, int cols) {
-  constexpr int VEC = Elem<T>::VEC;
-  float f[VEC];
-  Elem<T>::unpack(w, f);
+// The thread's VPT vectors of a row, as packed 16-byte words; zeros where
+// there is none.
+template <typename T, int VPT>
+__device__ __forceinline__ void load_vecs(const T* row, const Place& p, uint4* raw) {
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) f[k] = e + k >= 0 && e + k < cols ? f[k] : 0.0f;
-  return Elem<T>::pack(f);  // exact
+  for (int c = 0; c < VPT; ++c)
+    raw[c] = ld_stream_v4_if(row + col_of_vec<Elem<T>::VEC>(p, c), has_vec(p, c), 0u);
 }
 
-// The thread's VPT chunks of a row, as packed 16-byte words; zeros outside.
-// Shifted rows: a vector that crosses a row's end is loaded whole (its other
-// values belong to the neighbouring rows; mask_place() takes them out once
-// the loads are used, so that nothing waits here); only where that would
-// leave the buffer, at its first and last vector, are values loaded one at a
-// time.
-template <typename T, int VPT, bool ALIGNED>
-__device__ __forceinline__ void load_place(const RowOf<const T>& r, const Place& p, uint4* raw) {
-  constexpr int VEC = Elem<T>::VEC;
-#pragma unroll
-  for (int c = 0; c < VPT; ++c) {
-    const int e = col_at<VEC>(p, c, 0);
-    const T* const at = r.row + e;
-    if constexpr (ALIGNED) {
-      raw[c] = ld_stream_v4_if(at, e < p.cols, 0u);
-    } else {
-      const bool any = e + VEC > 0 && e < p.cols, inside = at >= r.begin && at + VEC <= r.end;
-      raw[c] = ld_stream_v4_if(at, any && inside, 0u);
-      if (any && !inside) {
-        float f[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          f[k] = e + k >= 0 && e + k < p.cols ? static_cast<float>(at[k]) : 0.0f;
-        raw[c] = Elem<T>::pack(f);  // exact
-      }
-    }
-  }
+// One value of the rows' type, and the rounding to it.
+template <typename T>
+__device__ __forceinline__ float load_one(const T* p) {
+  return static_cast<float>(*p);
 }
-
-// Zeros in place of what a shifted row's first and last vector hold of other
-// rows.
-template <typename T, int VPT, bool ALIGNED>
-__device__ __forceinline__ void mask_place(const Place& p, uint4* raw) {
-  if constexpr (!ALIGNED) {
-#pragma unroll
-    for (int c = 0; c < VPT; ++c) {
-      const int e = col_at<Elem<T>::VEC>(p, c, 0);
-      if (e < 0 || e + Elem<T>::VEC > p.cols) raw[c] = mask_edge<T>(raw[c], e, p.cols);
-    }
-  }
+template <typename T>
+__device__ __forceinline__ float round_one(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  return __bfloat162float(__float2bfloat16_rn(v));
 }
 
 // Stores that stay where they are written in program order: left to itself
@@ -135,125 +100,114 @@ __device__ __forceinline__ void st_v2(void* p, uint32_t x, uint32_t y) {
 __device__ __forceinline__ void st_v1(void* p, uint32_t x) {
   asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
 }
+__device__ __forceinline__ void st_u16(void* p, uint32_t x) {
+  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.global.u16 [%0], h;\n\t}" ::"l"(p), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_u8(void* p, uint32_t x) {
+  asm volatile("st.global.u8 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
 
-// One chunk stored in the rows' own type from its packed words.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void store_place(T* row, const Place& p, int c, uint4 w) {
-  constexpr int VEC = Elem<T>::VEC;
-  const int e = col_at<VEC>(p, c, 0);
-  if constexpr (ALIGNED) {
-    if (e < p.cols) st_v4(row + e, w);
-  } else {
-    if (e >= 0 && e + VEC <= p.cols) {
-      st_v4(row + e, w);
-    } else if (e + VEC > 0 && e < p.cols) {
-      float f[VEC];
-      Elem<T>::unpack(w, f);
+// Vector c stored in the rows' own type.
+template <typename T>
+__device__ __forceinline__ void store_vec(T* row, const Place& p, int c, uint4 w) {
+  if (has_vec(p, c)) st_v4(row + col_of_vec<Elem<T>::VEC>(p, c), w);
+}
+
+// Four or eight codes to any address, in the widest aligned pieces: s is the
+// address modulo 4 (the same for the whole row, so no lane waits for another).
+template <int W>
+__device__ __forceinline__ void store_unaligned(uint8_t* at, int s, const uint32_t* w) {
+  if (s == 0) {
 #pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        if (e + k >= 0 && e + k < p.cols) Elem<T>::store1(row + e + k, f[k]);  // exact
-    }
+    for (int k = 0; k < W; ++k) st_v1(at + 4 * k, w[k]);
+  } else if (s == 2) {
+    st_u16(at, w[0]);
+    if (W == 2) st_v1(at + 2, __funnelshift_r(w[0], w[W - 1], 16));
+    st_u16(at + 4 * W - 2, w[W - 1] >> 16);
+  } else if (s == 1) {
+    st_u8(at, w[0]);
+    st_u16(at + 1, w[0] >> 8);
+    if (W == 2) st_v1(at + 3, __funnelshift_r(w[0], w[W - 1], 24));
+    st_u8(at + 4 * W - 1, w[W - 1] >> 24);
+  } else {
+    st_u8(at, w[0]);
+    if (W == 2) st_v1(at + 1, __funnelshift_r(w[0], w[W - 1], 8));
+    st_u16(at + 4 * W - 3, w[W - 1] >> 8);
+    st_u8(at + 4 * W - 1, w[W - 1] >> 24);
   }
 }
 
-// Bytes first .. 3 of a word of codes whose first byte is column e.
-__device__ __forceinline__ void store_code_edge(uint8_t* row, int e, int cols, int first, uint32_t w) {
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-    if (b >= first && e + b >= 0 && e + b < cols) row[e + b] = static_cast<uint8_t>(w >> (8 * b));
-}
-
-// One chunk stored as codes (zeros for a row that is not finite).  Every lane
-// of the warp takes part.  Shifted rows: a lane's codes start s bytes past a
-// 4-byte boundary, the same s for the whole row; each lane writes the aligned
-// words that end in its own codes, the first of them completed by the last
-// codes of the lane before it.
+// Vector c stored as codes (zeros for a row that is not finite).
 template <typename T, int OUT, bool ALIGNED>
 __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, int c, const float* v, const RowScale& q) {
   constexpr int VEC = Elem<T>::VEC, W = VEC / 4;
-  const int e = col_at<VEC>(p, c, 0);
+  uint8_t* const at = row + col_of_vec<VEC>(p, c);
   uint32_t w[W];
 #pragma unroll
   for (int k = 0; k < W; ++k) w[k] = q.ok ? Code8<OUT>::pack4(v + 4 * k, q.inv) : 0u;
-  if constexpr (ALIGNED) {
-    if (e < p.cols) {
-      if constexpr (W == 2)
-        st_v2(row + e, w[0], w[1]);
-      else
-        st_v1(row + e, w[0]);
-    }
-  } else {
-    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row + e) & 3), lane = threadIdx.x & 31;
-    uint32_t before = __shfl_up_sync(0xffffffffu, w[W - 1], 1);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const uint32_t word = __funnelshift_l(before, w[k], 8 * s);
-      const int at = e - s + 4 * k;                     // column of the word's first byte
-      const int first = k == 0 && lane == 0 ? s : 0;    // the warp before wrote those
-      if (first == 0 && at >= 0 && at + 4 <= p.cols)
-        st_v1(row + at, word);
-      else if (at + 4 > 0 && at < p.cols)
-        store_code_edge(row, at, p.cols, first, word);
-      before = w[k];
-    }
-    if (lane == 31 && s != 0 && e + VEC - s < p.cols && e + VEC > 0)
-      store_code_edge(row, e + VEC - s, p.cols < e + VEC ? p.cols : e + VEC, 0, w[W - 1] >> (8 * (4 - s)));
-  }
+  if (!has_vec(p, c)) return;
+  if constexpr (!ALIGNED)
+    store_unaligned<W>(at, static_cast<int>(reinterpret_cast<uintptr_t>(at) & 3), w);
+  else if constexpr (W == 2)
+    st_v2(at, w[0], w[1]);
+  else
+    st_v1(at, w[0]);
 }
 
-// VEC fp32 parameters of chunk c (nullptr: ones), 16-byte aligned at column
+// VEC fp32 parameters of vector c (nullptr: ones), 16-byte aligned at column
 // 0.  The same for every row, so they come from L1 and L2.
 template <int VEC, bool ALIGNED>
 __device__ __forceinline__ void load_params(const float* g, const Place& p, int c, float* out) {
-  const int e = col_at<VEC>(p, c, 0);
+  const int e = col_of_vec<VEC>(p, c);
 #pragma unroll
   for (int k = 0; k < VEC; ++k) out[k] = 1.0f;
-  if (g == nullptr) return;
-  if constexpr (ALIGNED) {
-    if (e < p.cols) {
+  if (g == nullptr || !has_vec(p, c)) return;
+  // Shifted rows: the aligned groups of four around the vector, then a shift
+  // by r = e mod 4 (the same for the whole row): one of four copies runs.
+  const int r = ALIGNED ? 0 : e & 3, from = e - r;
+  float a[VEC + 4];
 #pragma unroll
-      for (int k = 0; k < VEC; k += 4) {
-        const float4 z = __ldg(reinterpret_cast<const float4*>(g + e + k));
-        out[k] = z.x;
-        out[k + 1] = z.y;
-        out[k + 2] = z.z;
-        out[k + 3] = z.w;
-      }
+  for (int k = 0; k < (ALIGNED ? VEC : VEC + 4); k += 4) {
+    float4 z = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    const int i = from + k;
+    if (ALIGNED || i + 4 <= p.cols) {
+      z = __ldg(reinterpret_cast<const float4*>(g + i));
+    } else if (i < p.cols) {
+      z.x = __ldg(g + i);
+      if (i + 1 < p.cols) z.y = __ldg(g + i + 1);
+      if (i + 2 < p.cols) z.z = __ldg(g + i + 2);
     }
+    a[k] = z.x;
+    a[k + 1] = z.y;
+    a[k + 2] = z.z;
+    a[k + 3] = z.w;
+  }
+  if (r == 0) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) out[k] = a[k];
+  } else if (r == 1) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) out[k] = a[k + 1];
+  } else if (r == 2) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) out[k] = a[k + 2];
   } else {
-    // the aligned groups of four around e, then a shift by r = e mod 4 (the
-    // same for the whole row)
-    const int r = e & 3, from = e - r;
-    float a[VEC + 4];
 #pragma unroll
-    for (int k = 0; k < VEC + 4; k += 4) {
-      float4 z = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-      const int i = from + k;  // a multiple of 4: a group before column 0 holds none of the row's
-      if (i >= 0 && i + 4 <= p.cols) {
-        z = __ldg(reinterpret_cast<const float4*>(g + i));
-      } else if (i >= 0 && i < p.cols) {
-        z.x = __ldg(g + i);
-        if (i + 1 < p.cols) z.y = __ldg(g + i + 1);
-        if (i + 2 < p.cols) z.z = __ldg(g + i + 2);
-      }
-      a[k] = z.x;
-      a[k + 1] = z.y;
-      a[k + 2] = z.z;
-      a[k + 3] = z.w;
-    }
-#pragma unroll
-    for (int k = 0; k < VEC + 2; ++k) a[k] = (r & 1) ? a[k + 1] : a[k];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) out[k] = (r & 2) ? a[k + 2] : a[k];
+    for (int k = 0; k < VEC; ++k) out[k] = a[k + 3];
   }
 }
 
-// Sum of s and NaN-propagating maximum of m over the team: a warp, or a block
-// of any number of warps (`red`: one pair per warp; one barrier).
-template <bool WARP>
+// Sum of s and NaN-propagating maximum of m over the team: LANES lanes of a
+// warp, or (LANES = 0) a block of any number of warps (`red`: one pair per
+// warp; one barrier).
+template <int LANES>
 __device__ __forceinline__ void team_sum_max(float& s, float& m, float2* red) {
-  warp_sum_max(s, m);
-  if constexpr (!WARP) {
+#pragma unroll
+  for (int o = (LANES == 0 ? 32 : LANES) / 2; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    m = absmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  if constexpr (LANES == 0) {
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(s, m);
     __syncthreads();
@@ -266,21 +220,52 @@ __device__ __forceinline__ void team_sum_max(float& s, float& m, float2* red) {
   }
 }
 
-// Calls fn(row, place) for the rows of this block: one row per warp, or one
-// per block at a time.
-template <bool WARP, typename F>
+// The maximum alone (of values: NaN if one is).
+template <int LANES>
+__device__ __forceinline__ void team_max(float& m, float* red) {
+  auto larger = [](float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  };
+#pragma unroll
+  for (int o = (LANES == 0 ? 32 : LANES) / 2; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if constexpr (LANES == 0) {
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = red[0];
+    for (int w = 1; w < warps; ++w) m = larger(m, red[w]);
+  }
+}
+
+// Calls fn(row, t, team, cols) for the rows of this block: 32 / LANES rows per
+// warp, or (LANES = 0) one per block at a time.  Lanes of a warp that have no
+// row left take part with no columns.
+template <int LANES, typename F>
 __device__ __forceinline__ void for_rows(size_t rows, int cols, F fn) {
-  if constexpr (WARP) {
-    const size_t per = blockDim.x >> 5, stride = gridDim.x * per;
-    const Place p = {static_cast<int>(threadIdx.x & 31), 32, cols, 0};
-    for (size_t row = blockIdx.x * per + (threadIdx.x >> 5); row < rows; row += stride) fn(row, p);
+  if constexpr (LANES > 0) {
+    constexpr int PER = 32 / LANES;
+    const size_t per = (blockDim.x >> 5) * PER, stride = gridDim.x * per;
+    const int lane = threadIdx.x & 31;
+    for (size_t first = blockIdx.x * per + (threadIdx.x >> 5) * PER; first < rows; first += stride) {
+      const size_t row = first + lane / LANES;
+      fn(row, lane % LANES, LANES, row < rows ? cols : 0);
+    }
   } else {
-    const Place p = {static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), cols, 0};
     for (size_t row = blockIdx.x; row < rows; row += gridDim.x) {
-      fn(row, p);
+      fn(row, static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), cols);
       if (row + gridDim.x < rows) __syncthreads();  // the reduction's scratch is used again
     }
   }
+}
+
+// Lanes a row of up to kRowWarpCols columns takes: eight values a lane where
+// that leaves lanes for another row (and, for shifted rows, a lane for each
+// value outside the vectors), else the whole warp.
+inline int row_lanes(size_t cols, bool aligned, int vec) {
+  if (cols <= 8 * kRowLaneEpt && (aligned || 2 * (vec - 1) <= 8)) return 8;
+  return cols <= 16 * kRowLaneEpt ? 16 : 32;
 }
 
 // Shape of a launch: threads per block, blocks.
@@ -288,19 +273,19 @@ struct RowLaunch {
   unsigned grid, threads;
 };
 
-// One warp per row: eight rows per block, halved down to two while blocks
-// would leave multiprocessors idle (as the softmax's warp path does).
-inline RowLaunch warp_launch(size_t rows) {
-  size_t per = kRowWarps;
-  while (per > 2 && (rows + per - 1) / per < 148) per /= 2;
-  const size_t blocks = (rows + per - 1) / per;
-  return {static_cast<unsigned>(blocks < kRowMaxGrid ? blocks : kRowMaxGrid), static_cast<unsigned>(32 * per)};
+// `lanes` lanes per row: eight warps per block, halved down to two while
+// blocks would leave multiprocessors idle (as the softmax's warp path does).
+inline RowLaunch warp_launch(size_t rows, int lanes) {
+  const size_t per_warp = 32 / lanes;
+  size_t warps = kRowWarps;
+  while (warps > 2 && (rows + warps * per_warp - 1) / (warps * per_warp) < 148) warps /= 2;
+  const size_t blocks = (rows + warps * per_warp - 1) / (warps * per_warp);
+  return {static_cast<unsigned>(blocks < kRowMaxGrid ? blocks : kRowMaxGrid), static_cast<unsigned>(32 * warps)};
 }
 
-// One block per row, as many warps as hold it at ept values a thread (`span`:
-// the columns, and the lead where rows are shifted).
-inline RowLaunch block_launch(size_t rows, size_t span, int ept) {
-  const size_t threads = ((span + ept - 1) / ept + 31) / 32 * 32;
+// One block per row, as many warps as hold it at ept values a thread.
+inline RowLaunch block_launch(size_t rows, size_t cols, int ept) {
+  const size_t threads = ((cols + ept - 1) / ept + 31) / 32 * 32;
   return {static_cast<unsigned>(rows < kRowMaxGrid ? rows : kRowMaxGrid), static_cast<unsigned>(threads)};
 }
 

@@ -14,54 +14,199 @@ namespace {
 constexpr int kStreamThreads = 512;
 constexpr size_t kMaxGrid = 0x7fffffffu;
 
+// Inputs are raised to this first: GELU there is under 1e-21 (erf form) and
+// 1e-35 (tanh form), and what the two forms exponentiate stays in range.
+// Exact in bf16.
+constexpr float kActFloor = -9.875f;
+constexpr uint32_t kActFloorPair = 0xc11ec11eu;
+
+// GELU of a pair to fp32 accuracy, as gelu_tanh_f2 / gelu_erf_f2, of values
+// not below kActFloor.  (The reciprocal on
+// the FMA pipes instead of MUFU, for all pairs or every other one: 46 and
+// 39.6 us against 38.2 for 16384 x 4096.)
+template <int EPI>
+__device__ __forceinline__ float2 act2(float2 x) {
+  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) {
+    const float2 a = mul2(x, fma2(splat2(kB), mul2(x, x), splat2(kA)));
+    const float2 s = add2(make_float2(ex2_ftz(a.x), ex2_ftz(a.y)), splat2(1.0f));
+    return mul2(x, make_float2(rcp_approx(s.x), rcp_approx(s.y)));
+  }
+  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) {
+    const float2 w = mul2(make_float2(fabsf(x.x), fabsf(x.y)), splat2(kRsqrt2));
+    const float2 s = fma2(splat2(0.5f), w, splat2(1.0f));
+    const float2 t = make_float2(rcp_approx(s.x), rcp_approx(s.y));
+    const float2 e = mul2(fma2(make_float2(-w.x, -w.y), w, erfc_poly(t)), splat2(kLog2e));
+    const float2 h = mul2(mul2(splat2(0.5f), t), make_float2(ex2_ftz(e.x), ex2_ftz(e.y)));
+    const float2 sg = make_float2(phi_sign(x.x), phi_sign(x.y));
+    return mul2(x, fma2(sg, h, fma2(sg, splat2(-0.5f), splat2(0.5f))));
+  }
+  return x;
+}
+
+// A packed word's values raised to kActFloor (NaN stays), where GELU follows.
+template <typename T, int EPI>
+__device__ __forceinline__ uint4 raised(uint4 w) {
+  if constexpr (EPI != FK_EPILOGUE_NONE && sizeof(T) == 4) {
+    w.x = __float_as_uint(max_nan(__uint_as_float(w.x), kActFloor));
+    w.y = __float_as_uint(max_nan(__uint_as_float(w.y), kActFloor));
+    w.z = __float_as_uint(max_nan(__uint_as_float(w.z), kActFloor));
+    w.w = __float_as_uint(max_nan(__uint_as_float(w.w), kActFloor));
+  } else if constexpr (EPI != FK_EPILOGUE_NONE) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(kActFloorPair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(kActFloorPair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.z) : "r"(kActFloorPair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w) : "r"(kActFloorPair));
+  }
+  return w;
+}
 template <int EPI>
 __device__ __forceinline__ float act(float x) {
-  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f<float>(x);
-  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f<float>(x);
-  return x;
+  return act2<EPI>(splat2(EPI == FK_EPILOGUE_NONE ? x : max_nan(x, kActFloor))).x;
+}
+
+// The largest |GELU(x)| of negative x is 0.1701 (either form), and GELU rises
+// from there on: where GELU of a row's largest value is above this, it is the
+// row's largest magnitude, and no other value's GELU is needed for the scale.
+constexpr float kGeluDip = 0.1725f;
+
+// Largest value (not magnitude) among m and a vector's, NaN if one is.
+template <typename T>
+__device__ __forceinline__ float max_words(float m, const uint4& w) {
+  if constexpr (sizeof(T) == 4) {
+    m = max_nan(max_nan(m, __uint_as_float(w.x)), __uint_as_float(w.y));
+    return max_nan(max_nan(m, __uint_as_float(w.z)), __uint_as_float(w.w));
+  } else {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return max_nan(max_nan(m, __uint_as_float(a << 16)), __uint_as_float(a & 0xffff0000u));
+  }
 }
 
 // ---------------------------------------------------------------- rows held in registers
 
-// Two values at a time (packed fp32 arithmetic).
-template <int EPI>
-__device__ __forceinline__ float2 act2(float2 x) {
-  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) return gelu_tanh_f2<float>(x);
-  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) return gelu_erf_f2<float>(x);
-  return x;
-}
-
-template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, bool WARP, int MAXT, int MINB>
+template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_constant__ QuantizeArgs a) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  __shared__ float2 red[WARP ? 1 : MAXT / 32];
+  __shared__ float red[LANES ? 1 : MAXT / 32];
   let_next_start();
   after_previous();
-  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, Place p) {
+  for_rows<LANES>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
     const size_t base = row * a.cols;
-    if (!ALIGNED) p.lead = lead_of(static_cast<const T*>(a.x) + base);
+    const T* const x = static_cast<const T*>(a.x) + base;
+    uint8_t* const o = static_cast<uint8_t*>(a.q) + base;
+    const Place p = place_of<T, ALIGNED>(t, team, cols, x);
+    const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
     uint4 raw[VPT];
-    load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.x), base, a.rows * a.cols), p, raw);
-    mask_place<T, VPT, ALIGNED>(p, raw);
-    float v[EPT], s = 0.0f, m = 0.0f;
+    load_vecs<T, VPT>(x, p, raw);
+    float ev = 0.0f;  // this thread's value outside the vectors
+    if (!ALIGNED && edge >= 0) ev = load_one(x + edge);
+    float v[EPT], m = 0.0f;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
-      Elem<T>::unpack(raw[c], v + c * VEC);
+      Elem<T>::unpack(raised<T, EPI>(raw[c]), v + c * VEC);
 #pragma unroll
       for (int k = 0; k < VEC; k += 2) {
-        const float2 z = act2<EPI>(make_float2(v[c * VEC + k], v[c * VEC + k + 1]));
+        const float2 x2 = make_float2(v[c * VEC + k], v[c * VEC + k + 1]);
+        const float2 z = act2<EPI>(x2);
         v[c * VEC + k] = z.x;
         v[c * VEC + k + 1] = z.y;
         m = absmax_nan(absmax_nan(m, z.x), z.y);
       }
     }
-    team_sum_max<WARP>(s, m, red);
+    if (!ALIGNED && edge >= 0) {
+      ev = act<EPI>(ev);
+      m = absmax_nan(m, ev);
+    }
+    team_max<LANES>(m, red);
     const RowScale q = row_scale<OUT>(m);
-    if (p.t == 0) a.scales[row] = q.scale;
+    if (t == 0 && cols > 0) a.scales[row] = q.scale;
 #pragma unroll
-    for (int c = 0; c < VPT; ++c)
-      store_codes<T, OUT, ALIGNED>(static_cast<uint8_t*>(a.q) + base, p, c, v + c * VEC, q);
+    for (int c = 0; c < VPT; ++c) store_codes<T, OUT, ALIGNED>(o, p, c, v + c * VEC, q);
+    if (!ALIGNED && edge >= 0) o[edge] = q.ok ? Code8<OUT>::pack1(ev, q.inv) : 0;
   });
+}
+
+// Wide rows: blocks that stay and walk the rows, the next row loaded before
+// the current one is computed.
+template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_constant__ QuantizeArgs a) {
+  constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
+  __shared__ float red[2][MAXT / 32], dip[MAXT / 32];
+  const int cols = static_cast<int>(a.cols), t = static_cast<int>(threadIdx.x), team = static_cast<int>(blockDim.x);
+  const T* const x = static_cast<const T*>(a.x);
+  let_next_start();
+  after_previous();
+  uint4 raw[VPT];
+  float ev = 0.0f;
+  if (blockIdx.x < a.rows) {
+    const T* const first = x + blockIdx.x * a.cols;
+    const Place p = place_of<T, ALIGNED>(t, team, cols, first);
+    load_vecs<T, VPT>(first, p, raw);
+    if (!ALIGNED && edge_col<VEC>(p) >= 0) ev = load_one(first + edge_col<VEC>(p));
+  }
+  int turn = 0;
+  for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const size_t base = row * a.cols;
+    const Place p = place_of<T, ALIGNED>(t, team, cols, x + base);
+    const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
+    uint4 next[VPT];
+    float nev = 0.0f;
+    if (row + gridDim.x < a.rows) {
+      const T* const nx = x + base + gridDim.x * a.cols;
+      const Place np = place_of<T, ALIGNED>(t, team, cols, nx);
+      load_vecs<T, VPT>(nx, np, next);
+      if (!ALIGNED && edge_col<VEC>(np) >= 0) nev = load_one(nx + edge_col<VEC>(np));
+    }
+    // the row's largest magnitude: for GELU, from its largest value alone
+    // where that decides, so that the values stay packed until their codes
+    // are made
+    float m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      if constexpr (EPI == FK_EPILOGUE_NONE) {
+        float f[VEC];
+        Elem<T>::unpack(raw[c], f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) m = absmax_nan(m, f[k]);
+      } else {
+        m = max_words<T>(m, raw[c]);
+      }
+    }
+    if (!ALIGNED && edge >= 0) m = EPI == FK_EPILOGUE_NONE ? absmax_nan(m, ev) : max_nan(m, ev);
+    team_max<0>(m, red[turn]);
+    if constexpr (EPI != FK_EPILOGUE_NONE) {
+      m = act<EPI>(m);
+      ev = act<EPI>(ev);
+      if (!(m > kGeluDip)) {  // small or negative values only, or a NaN: the same for the whole block
+        m = 0.0f;
+#pragma unroll 1
+        for (int j = t; j < cols; j += team) m = absmax_nan(m, act<EPI>(static_cast<float>(x[base + j])));
+        team_max<0>(m, dip);
+        __syncthreads();  // dip may be used by the next row
+      }
+    }
+    turn ^= 1;
+    const RowScale q = row_scale<OUT>(m);
+    uint8_t* const o = static_cast<uint8_t*>(a.q) + base;
+    if (t == 0) a.scales[row] = q.scale;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float f[VEC];
+      Elem<T>::unpack(raised<T, EPI>(raw[c]), f);
+#pragma unroll
+      for (int k = 0; k < VEC; k += 2) {
+        const float2 z = act2<EPI>(make_float2(f[k], f[k + 1]));
+        f[k] = z.x;
+        f[k + 1] = z.y;
+      }
+      store_codes<T, OUT, ALIGNED>(o, p, c, f, q);
+      raw[c] = next[c];
+    }
+    if (!ALIGNED && edge >= 0) o[edge] = q.ok ? Code8<OUT>::pack1(ev, q.inv) : 0;
+    ev = nev;
+  }
 }
 
 // ---------------------------------------------------------------- streaming path
@@ -90,31 +235,34 @@ __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(Quantiz
 
 template <typename T, int OUT, int EPI, bool ALIGNED>
 cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
-  const size_t span = row_span(a.cols, ALIGNED, Elem<T>::VEC);
-  if (span <= kRowWarpCols) {
-    const RowLaunch l = warp_launch(a.rows);
-    if (span <= kRowWarpCols / 4)
-      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 8, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-    else if (span <= kRowWarpCols / 2)
-      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-    else
-      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-  } else if (span <= kRowSmallCols) {
-    constexpr int EPT = 4 * Elem<T>::VEC;
-    const RowLaunch l = block_launch(a.rows, span, EPT);
-    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, EPT, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  } else if (span <= kRowLargeCols) {
-    const RowLaunch l = block_launch(a.rows, span, 32);
-    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  } else {
-    const RowLaunch l = block_launch(a.rows, span, 32);
-    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, false, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  if (a.cols <= kRowWarpCols) {
+    const int lanes = row_lanes(a.cols, ALIGNED, Elem<T>::VEC);
+    const RowLaunch l = warp_launch(a.rows, lanes);
+    if (lanes == 8)
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, kRowLaneEpt, ALIGNED, 8, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    if (lanes == 16)
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, kRowLaneEpt, ALIGNED, 16, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    if (a.cols <= kRowWarpCols / 4)
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 8, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    if (a.cols <= kRowWarpCols / 2)
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 16, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   }
+  const RowLaunch l = block_launch(a.rows, a.cols, 32);
+  if (sizeof(T) == 2 && a.cols > kRowBlockCols && a.cols <= kRowLargeCols) {
+    // as many blocks as stay resident: 1024 threads an SM at 64 registers
+    const unsigned fit = 148u * (1024u / l.threads);
+    return launch_overlapped(quantize_walk_kernel<T, OUT, EPI, 32, ALIGNED, 512, 2>, l.grid < fit ? l.grid : fit,
+                             l.threads, 0, 1, s, a);
+  }
+  if (a.cols <= kRowLargeCols)
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
+  return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
 }
 
 template <typename T, int OUT, int EPI>
 cudaError_t launch_epi(const QuantizeArgs& a, cudaStream_t s) {
-  if (row_span(a.cols, a.mode == kRowsAligned, Elem<T>::VEC) > kRowMaxCols) {
+  if (a.cols > kRowMaxCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     return launch_overlapped(quantize_stream_kernel<T, OUT, EPI>, g, kStreamThreads, 0, 1, s, a);
   }

@@ -18,45 +18,48 @@ namespace {
 constexpr int kStreamThreads = 512;
 constexpr size_t kMaxGrid = 0x7fffffffu;
 
-// One value of the sum, rounded to the rows' type.
-template <typename T>
-__device__ __forceinline__ float round_to(float v) {
-  if constexpr (sizeof(T) == 4) return v;
-  return __bfloat162float(__float2bfloat16_rn(v));
-}
-
 // ---------------------------------------------------------------- rows held in registers
 
 // MAXT, MINB: threads and blocks per SM the registers are sized for (64 a
 // thread for 1024 threads on an SM).
-template <typename T, int OUT, int EPT, bool ALIGNED, bool WARP, int MAXT, int MINB>
+template <typename T, int OUT, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_constant__ RmsnormArgs a) {
   constexpr bool Q8 = OUT == FK_I8 || OUT == FK_E4M3;
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  __shared__ float2 red[WARP ? 1 : MAXT / 32];
+  __shared__ float2 red[LANES ? 1 : MAXT / 32];
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   let_next_start();
   after_previous();
-  for_rows<WARP>(a.rows, static_cast<int>(a.cols), [&](size_t row, Place p) {
+  for_rows<LANES>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
     const size_t base = row * a.cols;
-    if (!ALIGNED) p.lead = lead_of(static_cast<const T*>(a.x) + base);
+    const T* const x = static_cast<const T*>(a.x) + base;
+    const T* const res = static_cast<const T*>(a.residual) + base;
+    T* const h = static_cast<T*>(a.h) + base;
+    const Place p = place_of<T, ALIGNED>(t, team, cols, x);
+    const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
     uint4 raw[VPT];
-    load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.x), base, a.rows * a.cols), p, raw);
+    load_vecs<T, VPT>(x, p, raw);
+    float ev = 0.0f, er = 0.0f;  // this thread's value outside the vectors
+    if (!ALIGNED && edge >= 0) ev = load_one(x + edge);
     if (a.residual) {
-      uint4 res[VPT];
-      load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.residual), base, a.rows * a.cols), p, res);
+      uint4 add[VPT];
+      load_vecs<T, VPT>(res, p, add);
+      if (!ALIGNED && edge >= 0) er = load_one(res + edge);
 #pragma unroll
       for (int c = 0; c < VPT; ++c) {
         float f[VEC], r[VEC];
         Elem<T>::unpack(raw[c], f);
-        Elem<T>::unpack(res[c], r);
+        Elem<T>::unpack(add[c], r);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) f[k] += r[k];
         raw[c] = Elem<T>::pack(f);  // h, rounded to the rows' type: what is normalised is what is stored
-        if (a.h) store_place<T, ALIGNED>(static_cast<T*>(a.h) + base, p, c, raw[c]);
+        if (a.h) store_vec(h, p, c, raw[c]);
+      }
+      if (!ALIGNED && edge >= 0) {
+        ev = round_one<T>(ev + er);
+        if (a.h) Elem<T>::store1(h + edge, ev);
       }
     }
-    mask_place<T, VPT, ALIGNED>(p, raw);
     float v[EPT], s = 0.0f, m = 0.0f;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -71,12 +74,17 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
         if (Q8) m = absmax_nan(m, f);
       }
     }
-    team_sum_max<WARP>(s, m, red);
+    if (!ALIGNED && edge >= 0) {
+      s = fmaf(ev, ev, s);
+      if (a.gamma) ev *= __ldg(a.gamma + edge);
+      if (Q8) m = absmax_nan(m, ev);
+    }
+    team_sum_max<LANES>(s, m, red);
     const float rstd = rms_rstd(s, inv_n, a.eps);
     RowScale q;
     if constexpr (Q8) {
       q = row_scale<OUT>(m * rstd);
-      if (p.t == 0) a.scales[row] = q.scale;
+      if (t == 0 && cols > 0) a.scales[row] = q.scale;
     }
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -86,7 +94,13 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
       if constexpr (Q8)
         store_codes<T, OUT, ALIGNED>(static_cast<uint8_t*>(a.y) + base, p, c, o, q);
       else
-        store_place<T, ALIGNED>(static_cast<T*>(a.y) + base, p, c, Elem<T>::pack(o));
+        store_vec(static_cast<T*>(a.y) + base, p, c, Elem<T>::pack(o));
+    }
+    if (!ALIGNED && edge >= 0) {
+      if constexpr (Q8)
+        (static_cast<uint8_t*>(a.y) + base)[edge] = q.ok ? Code8<OUT>::pack1(ev * rstd, q.inv) : 0;
+      else
+        Elem<T>::store1(static_cast<T*>(a.y) + base + edge, ev * rstd);
     }
   });
 }
@@ -111,7 +125,7 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
     float s = 0.0f, m = 0.0f;
     for (size_t j = threadIdx.x; j < cols; j += kStreamThreads) {
       float f = static_cast<float>(x[j]);
-      if (r) f = round_to<T>(f + static_cast<float>(r[j]));
+      if (r) f = round_one<T>(f + static_cast<float>(r[j]));
       if (h) h[j] = static_cast<T>(f);
       s = fmaf(f, f, s);
       if (Q8) m = absmax_nan(m, a.gamma ? f * a.gamma[j] : f);
@@ -130,7 +144,7 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
         f = static_cast<float>(h[j]);
       } else {
         f = static_cast<float>(x[j]);
-        if (r) f = round_to<T>(f + static_cast<float>(r[j]));
+        if (r) f = round_one<T>(f + static_cast<float>(r[j]));
       }
       const float v = (a.gamma ? f * a.gamma[j] : f) * rstd;
       if constexpr (Q8) {
@@ -145,31 +159,33 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
 
 template <typename T, int OUT, bool ALIGNED>
 cudaError_t launch_rows(const RmsnormArgs& a, cudaStream_t s) {
-  const size_t span = row_span(a.cols, ALIGNED, Elem<T>::VEC);
-  if (span <= kRowWarpCols) {
-    const RowLaunch l = warp_launch(a.rows);
-    if (span <= kRowWarpCols / 4)
-      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 8, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-    else if (span <= kRowWarpCols / 2)
-      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-    else
-      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, true, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
-  } else if (span <= kRowSmallCols) {
-    constexpr int EPT = 4 * Elem<T>::VEC;
-    const RowLaunch l = block_launch(a.rows, span, EPT);
-    return launch_overlapped(rmsnorm_row_kernel<T, OUT, EPT, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  } else if (span <= kRowLargeCols) {
-    const RowLaunch l = block_launch(a.rows, span, 32);
-    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  } else {
-    const RowLaunch l = block_launch(a.rows, span, 32);
-    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, false, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  if (a.cols <= kRowWarpCols) {
+    const int lanes = row_lanes(a.cols, ALIGNED, Elem<T>::VEC);
+    const RowLaunch l = warp_launch(a.rows, lanes);
+    if (lanes == 8)
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, kRowLaneEpt, ALIGNED, 8, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    if (lanes == 16)
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, kRowLaneEpt, ALIGNED, 16, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    if (a.cols <= kRowWarpCols / 4)
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 8, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    if (a.cols <= kRowWarpCols / 2)
+      return launch_overlapped(rmsnorm_row_kernel<T, OUT, 16, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   }
+  if (a.cols <= kRowBlockCols) {
+    constexpr int EPT = 4 * Elem<T>::VEC;
+    const RowLaunch l = block_launch(a.rows, a.cols, EPT);
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, EPT, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
+  }
+  const RowLaunch l = block_launch(a.rows, a.cols, 32);
+  if (a.cols <= kRowLargeCols)
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
+  return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
 }
 
 template <typename T, int OUT>
 cudaError_t launch_out(const RmsnormArgs& a, cudaStream_t s) {
-  if (a.mode == kRowsAny || row_span(a.cols, a.mode == kRowsAligned, Elem<T>::VEC) > kRowMaxCols) {
+  if (a.mode == kRowsAny || a.cols > kRowMaxCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     return launch_overlapped(rmsnorm_stream_kernel<T, OUT>, g, kStreamThreads, 0, 1, s, a);
   }

@@ -19,7 +19,7 @@ namespace {
 constexpr int kStreamThreads = 512;
 constexpr size_t kMaxGrid = 0x7fffffffu;
 constexpr int kColThreads = 128;      // columns per block of the column sums
-constexpr int kJoinCols = 32, kJoinWays = 16;
+constexpr int kJoinCols = 32, kJoinWays = 32;
 constexpr int kBwdEpt = 16;           // values a thread holds of a row (8 or 32 in a warp team where that fits better)
 constexpr int kBwdThreads = 512;
 constexpr size_t kBwdBlockCols = kBwdEpt * kBwdThreads;  // columns a block holds
@@ -32,7 +32,7 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 // (CL = 0: up to 1024 columns), a block (CL = 1: up to 8192), or a cluster of
 // CL blocks, so that a thread's columns never change: gamma and the running
 // dgamma sums live in its registers.  The next row's h and dy are loaded
-// before the current one is reduced (PF), which keeps HBM busy through the
+// before the current one is reduced, which keeps HBM busy through the
 // reduction.  At the end each block writes its columns' partial sums, one row
 // of workspace per team block (the warps of a warp-team block added first, in
 // order).
@@ -44,7 +44,7 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 // 8 values a thread 5.61.  8192 columns (one 512-thread block per SM) 5.86.
 // 16384 columns in one block: 3.4 TB/s at 32 values a thread, 3.0 with 1024
 // threads, hence the clusters.
-template <typename T, int EPT, bool ALIGNED, int CL, bool PF, int MAXT>
+template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   constexpr bool WARP = CL == 0;
@@ -55,43 +55,53 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
   const float inv_n = 1.0f / static_cast<float>(cols);
   const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  Place p = WARP ? Place{static_cast<int>(threadIdx.x & 31), 32, cols, 0}
-                 : Place{static_cast<int>(rank * blockDim.x + threadIdx.x), static_cast<int>(TEAMS * blockDim.x), cols, 0};
   const size_t team = WARP ? static_cast<size_t>(blockIdx.x) * warps + warp : blockIdx.x / TEAMS;
   const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps : gridDim.x / TEAMS;
   const T* const h = static_cast<const T*>(a.h);
   const T* const dy = static_cast<const T*>(a.dy);
-  // a team's rows are a multiple of eight apart (or it has one): their lead is the same
-  if (!ALIGNED) p.lead = lead_of(h + team * a.cols);
+  const T* const dres = static_cast<const T*>(a.dres);
+  // shifted rows: a team's rows are a multiple of eight apart (or it has one),
+  // so that all of them start alike
+  const Place p = place_of<T, ALIGNED>(WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(rank * blockDim.x + threadIdx.x),
+                                       WARP ? 32 : static_cast<int>(TEAMS * blockDim.x), cols, h + team * a.cols);
+  const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
   let_next_start();
   after_previous();
   if constexpr (CL > 1) cluster_arrive_relaxed();  // every block has started: waited for before the first push
   float gam[EPT], acc[EPT];
+  float eg = 1.0f, ea = 0.0f, eh = 0.0f, ed = 0.0f;  // gamma, sum, h and dy of this thread's column outside the vectors
+  if (!ALIGNED && edge >= 0 && a.gamma) eg = __ldg(a.gamma + edge);
 #pragma unroll
   for (int c = 0; c < VPT; ++c) load_params<VEC, ALIGNED>(a.gamma, p, c, gam + c * VEC);
 #pragma unroll
   for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
   uint4 rh[VPT], rd[VPT];
-  if (PF && team < a.rows) {
-    load_place<T, VPT, ALIGNED>(row_of(h, team * a.cols, a.rows * a.cols), p, rh);
-    load_place<T, VPT, ALIGNED>(row_of(dy, team * a.cols, a.rows * a.cols), p, rd);
+  if (team < a.rows) {
+    load_vecs<T, VPT>(h + team * a.cols, p, rh);
+    load_vecs<T, VPT>(dy + team * a.cols, p, rd);
+    if (!ALIGNED && edge >= 0) {
+      eh = load_one(h + team * a.cols + edge);
+      ed = load_one(dy + team * a.cols + edge);
+    }
   }
   if constexpr (CL > 1) cluster_wait();
   int turn = 0;
   for (size_t row = team; row < a.rows; row += stride) {
-    const size_t base = row * a.cols;
+    const size_t base = row * a.cols, next = base + stride * a.cols;
     uint4 nh[VPT], nd[VPT], rr[VPT];
-    if (!PF) {
-      load_place<T, VPT, ALIGNED>(row_of(h, base, a.rows * a.cols), p, rh);
-      load_place<T, VPT, ALIGNED>(row_of(dy, base, a.rows * a.cols), p, rd);
+    float neh = 0.0f, ned = 0.0f, er = 0.0f;
+    if (a.dres) {
+      load_vecs<T, VPT>(dres + base, p, rr);
+      if (!ALIGNED && edge >= 0) er = load_one(dres + base + edge);
     }
-    if (a.dres) load_place<T, VPT, ALIGNED>(row_of(static_cast<const T*>(a.dres), base, a.rows * a.cols), p, rr);
-    if (PF && row + stride < a.rows) {
-      load_place<T, VPT, ALIGNED>(row_of(h, base + stride * a.cols, a.rows * a.cols), p, nh);
-      load_place<T, VPT, ALIGNED>(row_of(dy, base + stride * a.cols, a.rows * a.cols), p, nd);
+    if (row + stride < a.rows) {
+      load_vecs<T, VPT>(h + next, p, nh);
+      load_vecs<T, VPT>(dy + next, p, nd);
+      if (!ALIGNED && edge >= 0) {
+        neh = load_one(h + next + edge);
+        ned = load_one(dy + next + edge);
+      }
     }
-    mask_place<T, VPT, ALIGNED>(p, rh);
-    mask_place<T, VPT, ALIGNED>(p, rd);
     float s = 0.0f, d = 0.0f;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -103,6 +113,10 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
         s = fmaf(f[k], f[k], s);
         d = fmaf(g[k] * gam[c * VEC + k], f[k], d);
       }
+    }
+    if (!ALIGNED && edge >= 0) {
+      s = fmaf(eh, eh, s);
+      d = fmaf(ed * eg, eh, d);
     }
     s = warp_sum(s);
     d = warp_sum(d);
@@ -141,41 +155,34 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < VEC; ++k) o[k] += q[k];
       }
-      store_place<T, ALIGNED>(static_cast<T*>(a.dx) + base, p, c, Elem<T>::pack(o));
+      store_vec(static_cast<T*>(a.dx) + base, p, c, Elem<T>::pack(o));
+      rh[c] = nh[c];
+      rd[c] = nd[c];
     }
-    if (PF) {
-#pragma unroll
-      for (int c = 0; c < VPT; ++c) {
-        rh[c] = nh[c];
-        rd[c] = nd[c];
-      }
+    if (!ALIGNED && edge >= 0) {
+      ea = fmaf(ed * eh, r, ea);
+      Elem<T>::store1(static_cast<T*>(a.dx) + base + edge, fmaf(r, ed * eg, -r3s * eh) + er);
+      eh = neh;
+      ed = ned;
     }
   }
   if (partial == nullptr) return;
   float* out = partial + static_cast<size_t>(blockIdx.x / TEAMS) * a.cols;
+  __shared__ float sums[WARP ? MAXT / 32 : 1][WARP ? 32 * EPT : 1];
+  float* const mine = WARP ? sums[warp] : out;
+#pragma unroll
+  for (int c = 0; c < VPT; ++c)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (has_vec(p, c)) mine[col_of_vec<VEC>(p, c) + k] = acc[c * VEC + k];
+  if (!ALIGNED && edge >= 0) mine[edge] = ea;
   if constexpr (WARP) {
-    __shared__ float sums[MAXT / 32][32 * EPT];
-#pragma unroll
-    for (int c = 0; c < VPT; ++c)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int e = col_at<VEC>(p, c, k);
-        if (e >= 0 && e < cols) sums[warp][e] = acc[c * VEC + k];
-      }
     __syncthreads();
     for (int e = threadIdx.x; e < cols; e += blockDim.x) {
       float v = sums[0][e];
       for (int w = 1; w < warps; ++w) v += sums[w][e];
       out[e] = v;
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < VPT; ++c)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int e = col_at<VEC>(p, c, k);
-        if (e >= 0 && e < cols) out[e] = acc[c * VEC + k];
-      }
   }
 }
 
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(kColThreads)
 }
 
 // dgamma_j = sum of the groups' partial sums: 32 columns per block, every
-// 16th group to each of its 16 warps, the warps' sums added in order.
+// 32nd group to each of its 32 warps, the warps' sums added in order.
 __global__ void __launch_bounds__(kJoinCols* kJoinWays)
     rmsnorm_bwd_join_kernel(const float* partial, float* dgamma, size_t cols, size_t groups) {
   __shared__ float part[kJoinWays][kJoinCols];
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kJoinCols* kJoinWays)
   let_next_start();
   after_previous();
   if (j < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (size_t g = way; g < groups; g += kJoinWays) acc += partial[g * cols + j];
   }
   part[way][lane] = acc;
@@ -310,13 +317,12 @@ struct BwdLaunch {
 };
 
 // Teams stay resident: as many blocks as fit the registers (128 a thread).
-// `span`: the columns, and the lead where rows are shifted; their teams then
-// walk rows a multiple of eight apart.
-BwdLaunch bwd_launch(size_t rows, size_t span, bool shifted) {
+// Shifted rows: teams walk rows a multiple of eight apart.
+BwdLaunch bwd_launch(size_t rows, size_t cols, bool shifted) {
   BwdLaunch l;
-  if (span <= static_cast<size_t>(kRowWarpCols)) {
+  if (cols <= static_cast<size_t>(kRowWarpCols)) {
     // a warp per row, 8 / 16 / 32 values a lane (about 80 / 110 / 200 registers: 3 / 2 / 1 blocks per SM)
-    l.ept = span <= 256 ? 8 : span <= 512 ? 16 : 32;
+    l.ept = cols <= 256 ? 8 : cols <= 512 ? 16 : 32;
     l.cluster = 0;
     l.threads = 32 * kRowWarps;
     const size_t fit = kSmCount * (l.ept == 8 ? 3 : l.ept == 16 ? 2 : 1), want = (rows + kRowWarps - 1) / kRowWarps;
@@ -324,9 +330,9 @@ BwdLaunch bwd_launch(size_t rows, size_t span, bool shifted) {
     return l;
   }
   l.ept = kBwdEpt;
-  l.cluster = span <= kBwdBlockCols ? 1 : span <= 2 * kBwdBlockCols ? 2 : 4;
+  l.cluster = cols <= kBwdBlockCols ? 1 : cols <= 2 * kBwdBlockCols ? 2 : 4;
   const size_t per = kBwdEpt * static_cast<size_t>(l.cluster);
-  l.threads = static_cast<int>(((span + per - 1) / per + 31) / 32 * 32);
+  l.threads = static_cast<int>(((cols + per - 1) / per + 31) / 32 * 32);
   const size_t fit = kSmCount / l.cluster * (l.cluster == 1 ? kBwdThreads / l.threads : 1);
   l.groups = rows < fit ? rows : shifted ? fit / 8 * 8 : fit;
   l.blocks = l.groups * l.cluster;
@@ -335,14 +341,14 @@ BwdLaunch bwd_launch(size_t rows, size_t span, bool shifted) {
 
 template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
 cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, true, MAXT>,
+  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, MAXT>,
                            static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), 0, CL > 1 ? CL : 1, s, a,
                            partial);
 }
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
-  const BwdLaunch l = bwd_launch(a.rows, row_span(a.cols, ALIGNED, Elem<T>::VEC), !ALIGNED);
+  const BwdLaunch l = bwd_launch(a.rows, a.cols, !ALIGNED);
   float* partial = a.dgamma ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaErrorInvalidValue;
   if (l.cluster == 0) {
@@ -361,7 +367,7 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
   // rows too long for a cluster's registers, or buffers that lie differently
-  if (a.mode == kRowsAny || row_span(a.cols, a.mode == kRowsAligned, Elem<T>::VEC) > 4 * kBwdBlockCols)
+  if (a.mode == kRowsAny || a.cols > 4 * kBwdBlockCols)
     return launch_stream<T>(a, ws, s);
   return a.mode == kRowsAligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
 }
@@ -372,9 +378,9 @@ cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
   const size_t stream = stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
   if (cols > 4 * kBwdBlockCols || !want_dgamma) return stream;
-  const size_t span = row_span(cols, false, vec_elems(dtype));
+  (void)dtype;
   size_t groups = bwd_launch(rows, cols, false).groups;
-  const size_t shifted = bwd_launch(rows, span, true).groups;
+  const size_t shifted = bwd_launch(rows, cols, true).groups;
   if (shifted > groups) groups = shifted;
   const size_t rowed = groups * cols * sizeof(float);
   return rowed > stream ? rowed : stream;

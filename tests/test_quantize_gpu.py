@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(37, 1), (3, 7), (65, 64), (33, 1000), (17, 1024), (17, 1025), (9, 2048), (9, 2049), (6, 4096), (3, 11008),
           (3, 16384), (2, 16385), (2, 32768), (2, 32769), (2, 100003), (1, 262144), (1300, 256), (700, 1000), (900, 4096),
           (9, 1), (9, 2), (9, 5), (9, 9), (9, 31), (9, 253), (9, 257), (9, 509), (9, 1017), (9, 1021), (9, 2047), (9, 4091),
-          (9, 4093), (9, 8193), (9, 16381), (9, 32761), (9, 32765)]
+          (9, 4093), (9, 8193), (9, 16381), (9, 32761), (9, 32765),
+          (5003, 64), (5001, 61), (333, 57), (2999, 128), (2999, 122), (7, 128), (1, 48), (3, 113)]
 
 
 @pytest.fixture(scope="module")

@@ -84,7 +84,8 @@ def test_forward(fk, torch_mod, rows, cols, dtype, out):
 @pytest.mark.parametrize("out", [None, "e4m3"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols", [(1, 256), (149, 256), (1200, 256), (2400, 512), (1, 4096), (300, 4096),
-                                       (1500, 4096), (701, 1003), (4000, 129)])
+                                       (1500, 4096), (701, 1003), (4000, 129), (5003, 64),
+                                       (5001, 63), (333, 57), (2999, 128), (2999, 122), (7, 128), (1, 48), (3, 113)])
 def test_many_rows(fk, torch_mod, rows, cols, dtype, out):
     """Row counts on both sides of what fills the GPU (kernel shapes depend on it)."""
     x, r = make_rows(rows, cols, dtype, rows), make_rows(rows, cols, dtype, rows + 1)
