@@ -23,14 +23,17 @@ constexpr int kJoinCols = 32, kJoinWays = 32;
 constexpr int kBwdEpt = 16;           // values a thread holds of a row (8 or 32 in a warp team where that fits better)
 constexpr int kBwdThreads = 512;
 constexpr size_t kBwdBlockCols = kBwdEpt * kBwdThreads;  // columns a block holds
+// Blocks per SM of warp teams with 8 values a lane (registers follow): 200000 x
+// 64 fp32 29 us at three and 35 at four, 100000 x 128 bf16 27 and 25.
+constexpr int small_blocks(int vec) { return vec == 8 ? 4 : 3; }
 constexpr int kSmCount = 148;
 constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 
 // ---------------------------------------------------------------- rows held in registers
 
-// Blocks that stay on the GPU and walk the rows.  The team of a row is a warp
-// (CL = 0: up to 1024 columns), a block (CL = 1: up to 8192), or a cluster of
-// CL blocks, so that a thread's columns never change: gamma and the running
+// Blocks that stay on the GPU and walk the rows.  The team of a row is LANES
+// lanes of a warp (up to 1024 columns), or (LANES = 0) the CL blocks of a
+// cluster (one up to 8192 columns), so that a thread's columns never change: gamma and the running
 // dgamma sums live in its registers.  The next row's h and dy are loaded
 // before the current one is reduced, which keeps HBM busy through the
 // reduction.  At the end each block writes its columns' partial sums, one row
@@ -44,10 +47,11 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 // 8 values a thread 5.61.  8192 columns (one 512-thread block per SM) 5.86.
 // 16384 columns in one block: 3.4 TB/s at 32 values a thread, 3.0 with 1024
 // threads, hence the clusters.
-template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
+template <typename T, int EPT, bool ALIGNED, int LANES, int CL, int MAXT>
+__global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 ? 2 : small_blocks(Elem<T>::VEC)) rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  constexpr bool WARP = CL == 0;
+  constexpr bool WARP = LANES > 0;
+  constexpr int PER = WARP ? 32 / (WARP ? LANES : 1) : 1;  // rows a warp takes at a time
   constexpr int TEAMS = CL > 1 ? CL : 1;
   // two scratch rows in turn, one pair per warp of the team: one barrier a row
   __shared__ float2 red[2][WARP ? 1 : TEAMS * (MAXT / 32)];
@@ -55,15 +59,17 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
   const float inv_n = 1.0f / static_cast<float>(cols);
   const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const size_t team = WARP ? static_cast<size_t>(blockIdx.x) * warps + warp : blockIdx.x / TEAMS;
-  const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps : gridDim.x / TEAMS;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const size_t team = WARP ? (static_cast<size_t>(blockIdx.x) * warps + warp) * PER + lane / (WARP ? LANES : 32)
+                           : blockIdx.x / TEAMS;
+  const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps * PER : gridDim.x / TEAMS;
   const T* const h = static_cast<const T*>(a.h);
   const T* const dy = static_cast<const T*>(a.dy);
   const T* const dres = static_cast<const T*>(a.dres);
   // shifted rows: a team's rows are a multiple of eight apart (or it has one),
   // so that all of them start alike
-  const Place p = place_of<T, ALIGNED>(WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(rank * blockDim.x + threadIdx.x),
-                                       WARP ? 32 : static_cast<int>(TEAMS * blockDim.x), cols, h + team * a.cols);
+  const Place p = place_of<T, ALIGNED>(WARP ? lane % (WARP ? LANES : 32) : static_cast<int>(rank * blockDim.x + threadIdx.x),
+                                       WARP ? LANES : static_cast<int>(TEAMS * blockDim.x), cols, h + team * a.cols);
   const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
   let_next_start();
   after_previous();
@@ -76,6 +82,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
   uint4 rh[VPT], rd[VPT];
+#pragma unroll
+  for (int c = 0; c < VPT; ++c) rh[c] = rd[c] = make_uint4(0u, 0u, 0u, 0u);
   if (team < a.rows) {
     load_vecs<T, VPT>(h + team * a.cols, p, rh);
     load_vecs<T, VPT>(dy + team * a.cols, p, rd);
@@ -86,11 +94,13 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
   }
   if constexpr (CL > 1) cluster_wait();
   int turn = 0;
-  for (size_t row = team; row < a.rows; row += stride) {
+  // (a warp's teams go on together until the last of them has no row left)
+  for (size_t row = team; row - lane / (WARP ? LANES : 32) < a.rows; row += stride) {
     const size_t base = row * a.cols, next = base + stride * a.cols;
+    const bool live = !WARP || row < a.rows;
     uint4 nh[VPT], nd[VPT], rr[VPT];
     float neh = 0.0f, ned = 0.0f, er = 0.0f;
-    if (a.dres) {
+    if (a.dres && live) {
       load_vecs<T, VPT>(dres + base, p, rr);
       if (!ALIGNED && edge >= 0) er = load_one(dres + base + edge);
     }
@@ -118,15 +128,17 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
       s = fmaf(eh, eh, s);
       d = fmaf(ed * eg, eh, d);
     }
-    s = warp_sum(s);
-    d = warp_sum(d);
+#pragma unroll
+    for (int o = (WARP ? LANES : 32) / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      d += __shfl_xor_sync(0xffffffffu, d, o);
+    }
     if constexpr (!WARP) {
       if constexpr (CL > 1) {
-        if ((threadIdx.x & 31) < TEAMS)
-          st_cluster_f2(cluster_addr(&red[turn][rank * warps + warp], threadIdx.x & 31), s, d);
+        if (lane < TEAMS) st_cluster_f2(cluster_addr(&red[turn][rank * warps + warp], lane), s, d);
         cluster_barrier();
       } else {
-        if ((threadIdx.x & 31) == 0) red[turn][warp] = make_float2(s, d);
+        if (lane == 0) red[turn][warp] = make_float2(s, d);
         __syncthreads();
       }
       s = red[turn][0].x;
@@ -139,6 +151,7 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
     }
     const float r = rms_rstd(s, inv_n, a.eps);
     const float r3s = r * r * r * (d * inv_n);
+    if (!live) break;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
       float f[VEC], g[VEC], o[VEC];
@@ -168,8 +181,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
   }
   if (partial == nullptr) return;
   float* out = partial + static_cast<size_t>(blockIdx.x / TEAMS) * a.cols;
-  __shared__ float sums[WARP ? MAXT / 32 : 1][WARP ? 32 * EPT : 1];
-  float* const mine = WARP ? sums[warp] : out;
+  __shared__ float sums[WARP ? MAXT / 32 * PER : 1][WARP ? LANES * EPT : 1];
+  float* const mine = WARP ? sums[threadIdx.x / (WARP ? LANES : 1)] : out;
 #pragma unroll
   for (int c = 0; c < VPT; ++c)
 #pragma unroll
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_bwd_row_kernel(const __grid_c
     __syncthreads();
     for (int e = threadIdx.x; e < cols; e += blockDim.x) {
       float v = sums[0][e];
-      for (int w = 1; w < warps; ++w) v += sums[w][e];
+      for (int w = 1; w < warps * PER; ++w) v += sums[w][e];
       out[e] = v;
     }
   }
@@ -312,23 +325,26 @@ cudaError_t launch_stream(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 // How the registers-resident kernel is launched for a shape: blocks, threads,
 // blocks per team, rows of partial sums.
 struct BwdLaunch {
-  int ept, cluster, threads;
+  int lanes, ept, cluster, threads;
   size_t blocks, groups;
 };
 
 // Teams stay resident: as many blocks as fit the registers (128 a thread).
 // Shifted rows: teams walk rows a multiple of eight apart.
-BwdLaunch bwd_launch(size_t rows, size_t cols, bool shifted) {
+BwdLaunch bwd_launch(size_t rows, size_t cols, int vec, bool shifted) {
   BwdLaunch l;
   if (cols <= static_cast<size_t>(kRowWarpCols)) {
-    // a warp per row, 8 / 16 / 32 values a lane (about 80 / 110 / 200 registers: 3 / 2 / 1 blocks per SM)
+    // a warp or less per row, 8 / 16 / 32 values a lane
+    l.lanes = row_lanes(cols, !shifted, vec);
     l.ept = cols <= 256 ? 8 : cols <= 512 ? 16 : 32;
     l.cluster = 0;
     l.threads = 32 * kRowWarps;
-    const size_t fit = kSmCount * (l.ept == 8 ? 3 : l.ept == 16 ? 2 : 1), want = (rows + kRowWarps - 1) / kRowWarps;
+    const size_t per = static_cast<size_t>(kRowWarps) * (32 / l.lanes);
+    const size_t fit = kSmCount * (l.ept == 8 ? small_blocks(vec) : l.ept == 16 ? 2 : 1), want = (rows + per - 1) / per;
     l.blocks = l.groups = want < fit ? want : fit;
     return l;
   }
+  l.lanes = 0;
   l.ept = kBwdEpt;
   l.cluster = cols <= kBwdBlockCols ? 1 : cols <= 2 * kBwdBlockCols ? 2 : 4;
   const size_t per = kBwdEpt * static_cast<size_t>(l.cluster);
@@ -339,26 +355,28 @@ BwdLaunch bwd_launch(size_t rows, size_t cols, bool shifted) {
   return l;
 }
 
-template <typename T, int EPT, bool ALIGNED, int CL, int MAXT>
+template <typename T, int EPT, bool ALIGNED, int LANES, int CL, int MAXT>
 cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, CL, MAXT>,
+  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, LANES, CL, MAXT>,
                            static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), 0, CL > 1 ? CL : 1, s, a,
                            partial);
 }
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
-  const BwdLaunch l = bwd_launch(a.rows, a.cols, !ALIGNED);
+  const BwdLaunch l = bwd_launch(a.rows, a.cols, Elem<T>::VEC, !ALIGNED);
   float* partial = a.dgamma ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaErrorInvalidValue;
-  if (l.cluster == 0) {
-    if (l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 0, 256>(a, partial, l, s);
-    if (l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 0, 256>(a, partial, l, s);
-    if (l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 0, 256>(a, partial, l, s);
+  if (l.lanes > 0) {
+    if (l.lanes == 8) e = launch_row_kernel<T, 8, ALIGNED, 8, 1, 256>(a, partial, l, s);
+    if (l.lanes == 16) e = launch_row_kernel<T, 8, ALIGNED, 16, 1, 256>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 32, 1, 256>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 32, 1, 256>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 32, 1, 256>(a, partial, l, s);
   } else {
-    if (l.cluster == 1) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 1, kBwdThreads>(a, partial, l, s);
-    if (l.cluster == 2) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 2, kBwdThreads>(a, partial, l, s);
-    if (l.cluster == 4) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 4, kBwdThreads>(a, partial, l, s);
+    if (l.cluster == 1) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, 1, kBwdThreads>(a, partial, l, s);
+    if (l.cluster == 2) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, 2, kBwdThreads>(a, partial, l, s);
+    if (l.cluster == 4) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, 4, kBwdThreads>(a, partial, l, s);
   }
   if (e != cudaSuccess || partial == nullptr) return e;
   return launch_join(partial, a.dgamma, a.cols, l.groups, s);
@@ -378,9 +396,8 @@ cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
   const size_t stream = stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
   if (cols > 4 * kBwdBlockCols || !want_dgamma) return stream;
-  (void)dtype;
-  size_t groups = bwd_launch(rows, cols, false).groups;
-  const size_t shifted = bwd_launch(rows, cols, true).groups;
+  size_t groups = bwd_launch(rows, cols, vec_elems(dtype), false).groups;
+  const size_t shifted = bwd_launch(rows, cols, vec_elems(dtype), true).groups;
   if (shifted > groups) groups = shifted;
   const size_t rowed = groups * cols * sizeof(float);
   return rowed > stream ? rowed : stream;

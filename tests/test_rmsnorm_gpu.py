@@ -217,7 +217,8 @@ def check_backward(dy, h, gamma, dres, got, eps=1e-6):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols", SHAPES + [(300, 64), (1200, 1000), (999, 4096), (150, 8192), (130, 16384), (999, 2047), (3001, 255),
-                                                (1300, 511), (1201, 1001), (170, 8193), (90, 20001)])
+                                                (1300, 511), (1201, 1001), (170, 8193), (90, 20001), (5003, 64), (20001, 61),
+                                                (333, 57), (9001, 128), (9001, 122), (7, 128), (1, 48)])
 def test_backward(fk, torch_mod, rows, cols, dtype):
     dy, h, dr = (make_rows(rows, cols, dtype, cols + i, 0.3) for i in range(3))
     g = gamma_of(cols, cols)
