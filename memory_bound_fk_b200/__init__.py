@@ -396,7 +396,7 @@ def _stream_handle(t) -> int:
 
 
 def _check_tensor(t, name: str):
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -567,16 +567,23 @@ def attention(q, k, v, causal: bool = True, scale: float | None = None, out=None
 
 
 # ---------------------------------------------------------------- the 8-bit linear layer
+#
+# At decode sizes the host side of a call outlasts its kernel, so these
+# helpers look up what they need of torch once, test operands in line and
+# leave the wording of a refusal to _like().
 
-_Q8_TYPES: dict = {}    # torch.int8 / torch.float8_e4m3fn -> fk_q8type, filled at first use
+_torch = None           # the torch module, at first use
+_FLOAT_CODES: dict = {}  # torch.float32 / torch.bfloat16 -> fk_dtype
+_Q8_CODES: dict = {}     # torch.int8 / torch.float8_e4m3fn -> fk_q8type
 
 
-def _q8_code(dt):
-    """fk_q8type of a torch dtype, or None."""
-    if not _Q8_TYPES:
-        import torch
-        _Q8_TYPES.update({torch.int8: FK_I8, torch.float8_e4m3fn: FK_E4M3})
-    return _Q8_TYPES.get(dt)
+def _load_torch():
+    global _torch
+    import torch
+    _FLOAT_CODES.update({torch.float32: FK_F32, torch.bfloat16: FK_BF16})
+    _Q8_CODES.update({torch.int8: FK_I8, torch.float8_e4m3fn: FK_E4M3})
+    _torch = torch
+    return torch
 
 
 def _like(t, name: str, shape, dtype, device: int) -> int:
@@ -590,11 +597,17 @@ def _like(t, name: str, shape, dtype, device: int) -> int:
     return t.data_ptr()
 
 
-def _rows_of(x, name: str) -> tuple[int, int]:
-    if x.dim() == 0:
+def _rows_input(x, name: str):
+    """(fk_dtype, shape, rows, columns) of a contiguous fp32/bf16 CUDA tensor."""
+    _check_tensor(x, name)
+    code = _FLOAT_CODES.get(x.dtype)
+    if code is None:
+        raise TypeError("fk operators take float32 or bfloat16")
+    shape = x.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    cols = x.shape[-1]
-    return (x.numel() // cols if cols else 0), cols
+    cols = shape[-1]
+    return code, shape, (x.numel() // cols if cols else 0), cols
 
 
 def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out_dtype=None, out=None, scales=None,
@@ -607,35 +620,35 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out_dtype=None, ou
     8-bit codes with one fp32 scale per row.  Returns y, or (codes, scales);
     with a residual, h comes last: (y, h) or (codes, scales, h).  weight: fp32,
     x.shape[-1] values.  residual_out may be residual or x (updated in place)."""
-    import torch
-    _check_tensor(x, "x")
-    code = _dtype_code(x.dtype)
-    shape, dtype, dev = x.shape, x.dtype, x.get_device()
-    rows, cols = _rows_of(x, "x")
-    lead = shape[:-1]
+    torch = _torch or _load_torch()
+    code, shape, rows, cols = _rows_input(x, "x")
+    dtype, dev = x.dtype, x.get_device()
     if out_dtype is None:
         out_dtype = dtype if out is None else out.dtype
-    q8 = _q8_code(out_dtype)
-    if q8 is None and out_dtype != dtype:
-        raise TypeError("out_dtype must be x's dtype, torch.int8 or torch.float8_e4m3fn")
-    if q8 is None and scales is not None:
-        raise ValueError("scales belong to 8-bit outputs")
-    if q8 is not None and cols == 0:
-        raise ValueError("rows without columns have no scale")
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out needs a residual")
+    q8 = _Q8_CODES.get(out_dtype)
+    p_scales = p_h = 0
     # what is made here needs no checks
     if out is None:
         out = torch.empty_like(x, dtype=out_dtype)
         p_out = out.data_ptr()
     else:
         p_out = _like(out, "out", shape, out_dtype, dev)
-    if q8 is not None and scales is None:
-        scales = x.new_empty(lead, dtype=torch.float32)
+    if q8 is None:
+        if out_dtype is not dtype:
+            raise TypeError("out_dtype must be x's dtype, torch.int8 or torch.float8_e4m3fn")
+        if scales is not None:
+            raise ValueError("scales belong to 8-bit outputs")
+    elif cols == 0:
+        raise ValueError("rows without columns have no scale")
+    elif scales is None:
+        scales = x.new_empty(shape[:-1], dtype=torch.float32)
         p_scales = scales.data_ptr()
     else:
-        p_scales = _like(scales, "scales", lead, torch.float32, dev)
-    if residual is not None and residual_out is None:
+        p_scales = _like(scales, "scales", shape[:-1], torch.float32, dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    elif residual_out is None:
         residual_out = torch.empty_like(x)
         p_h = residual_out.data_ptr()
     else:
@@ -660,24 +673,27 @@ def rmsnorm_backward(dy, h, weight=None, eps: float = 1e-6, dresidual=None, out=
     written over dy, h or dresidual (out=).  dweight is fp32, None when
     need_dweight is false.  `workspace` (a CUDA tensor of at least
     fk_rmsnorm_rows_bwd_workspace bytes) makes the call allocation-free."""
-    import torch
-    _check_tensor(h, "h")
-    code = _dtype_code(h.dtype)
-    rows, cols = _rows_of(h, "h")
-    shape, dtype, dev = h.shape, h.dtype, h.get_device()
+    torch = _torch or _load_torch()
+    code, shape, rows, cols = _rows_input(h, "h")
+    dtype, dev = h.dtype, h.get_device()
+    p_dw = 0
     if not need_dweight:
         if dweight is not None:
             raise ValueError("dweight given, but need_dweight is false")
     elif dweight is None:
         dweight = h.new_empty((cols,), dtype=torch.float32)
+        p_dw = dweight.data_ptr()
+    else:
+        p_dw = _like(dweight, "dweight", (cols,), torch.float32, dev)
     if out is None:
         out = torch.empty_like(h)
+        p_out = out.data_ptr()
+    else:
+        p_out = _like(out, "out", shape, dtype, dev)
     if dy is None:
         raise TypeError("dy must be a CUDA tensor")
-    args = (_like(dy, "dy", shape, dtype, dev), h.data_ptr(),
-            _like(weight, "weight", (cols,), torch.float32, dev), _like(dresidual, "dresidual", shape, dtype, dev),
-            _like(out, "out", shape, dtype, dev), _like(dweight, "dweight", (cols,), torch.float32, dev), rows,
-            cols, code, eps)
+    args = (_like(dy, "dy", shape, dtype, dev), h.data_ptr(), _like(weight, "weight", (cols,), torch.float32, dev),
+            _like(dresidual, "dresidual", shape, dtype, dev), p_out, p_dw, rows, cols, code, eps)
     if workspace is None:
         st = lib().fk_rmsnorm_rows_bwd(*args, _stream_handle(h))
     else:
@@ -695,28 +711,29 @@ def quantize_rows(x, dtype=None, gelu: str | None = None, out=None, scales=None)
     being the values.  dtype: torch.int8 (default) or torch.float8_e4m3fn;
     gelu: None, "tanh" or "erf" (or torch's "none", the exact form), applied
     first."""
-    import torch
-    _check_tensor(x, "x")
-    code = _dtype_code(x.dtype)
-    if gelu not in _EPILOGUES:
+    torch = _torch or _load_torch()
+    code, shape, rows, cols = _rows_input(x, "x")
+    epilogue = _EPILOGUES.get(gelu)
+    if epilogue is None:
         raise ValueError("gelu must be None, 'tanh' or 'erf'")
-    rows, cols = _rows_of(x, "x")
     if cols == 0:
         raise ValueError("rows without columns have no scale")
     if dtype is None:
         dtype = torch.int8 if out is None else out.dtype
-    q8 = _q8_code(dtype)
+    q8 = _Q8_CODES.get(dtype)
     if q8 is None:
         raise TypeError("dtype must be torch.int8 or torch.float8_e4m3fn")
     if out is None:
         out = torch.empty_like(x, dtype=dtype)
-    shape, dev = x.shape, x.get_device()
-    lead = shape[:-1]
+        p_out = out.data_ptr()
+    else:
+        p_out = _like(out, "out", shape, dtype, x.get_device())
     if scales is None:
-        scales = x.new_empty(lead, dtype=torch.float32)
-    st = lib().fk_quantize_rows(x.data_ptr(), _like(out, "out", shape, dtype, dev),
-                                _like(scales, "scales", lead, torch.float32, dev), rows, cols, code, q8,
-                                _EPILOGUES[gelu], _stream_handle(x))
+        scales = x.new_empty(shape[:-1], dtype=torch.float32)
+        p_scales = scales.data_ptr()
+    else:
+        p_scales = _like(scales, "scales", shape[:-1], torch.float32, x.get_device())
+    st = lib().fk_quantize_rows(x.data_ptr(), p_out, p_scales, rows, cols, code, q8, epilogue, _stream_handle(x))
     if st != FK_OK:
         raise FkError(st, "fk_quantize_rows")
     return out, scales
@@ -731,28 +748,35 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, gelu: str | None = None, out_
     out_dtype (bfloat16 by default, or float32).  `workspace` (a CUDA tensor
     of at least fk_matmul_q8_workspace bytes) makes a call that needs one
     allocation-free."""
-    import torch
+    torch = _torch or _load_torch()
     _check_tensor(a, "a")
     _check_tensor(b, "b")
-    q8 = _q8_code(a.dtype)
-    if q8 is None or b.dtype != a.dtype:
+    q8 = _Q8_CODES.get(a.dtype)
+    if q8 is None or b.dtype is not a.dtype:
         raise TypeError("a and b must both be torch.int8 or both torch.float8_e4m3fn")
-    if a.dim() == 0 or b.dim() != 2 or b.shape[1] != a.shape[-1] or b.get_device() != a.get_device():
+    shape, dev, f32 = a.shape, a.get_device(), torch.float32
+    if not shape or b.dim() != 2 or b.shape[1] != shape[-1] or b.get_device() != dev:
         raise ValueError("a is [..., k] and b is [n, k], on one device")
-    if gelu not in _EPILOGUES:
+    epilogue = _EPILOGUES.get(gelu)
+    if epilogue is None:
         raise ValueError("gelu must be None, 'tanh' or 'erf'")
     n, k = b.shape
-    lead, dev = a.shape[:-1], a.get_device()
+    lead = shape[:-1]
     if a_scales is None or b_scales is None:
         raise TypeError("a_scales and b_scales must be CUDA tensors")
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
+    out_code = _FLOAT_CODES.get(out_dtype)
+    if out_code is None:
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     if out is None:
         out = a.new_empty((*lead, n), dtype=out_dtype)
-    m = lead.numel()
-    args = (a.data_ptr(), b.data_ptr(), _like(a_scales, "a_scales", lead, torch.float32, dev),
-            _like(b_scales, "b_scales", (n,), torch.float32, dev), _like(bias, "bias", (n,), torch.float32, dev),
-            _like(out, "out", (*lead, n), out_dtype, dev), m, n, k, q8, _dtype_code(out_dtype), _EPILOGUES[gelu])
+        p_out = out.data_ptr()
+    else:
+        p_out = _like(out, "out", (*lead, n), out_dtype, dev)
+    args = (a.data_ptr(), b.data_ptr(), _like(a_scales, "a_scales", lead, f32, dev),
+            _like(b_scales, "b_scales", (n,), f32, dev), _like(bias, "bias", (n,), f32, dev), p_out, lead.numel(), n, k,
+            q8, out_code, epilogue)
     if workspace is None:
         st = lib().fk_matmul_q8(*args, _stream_handle(a))
     else:

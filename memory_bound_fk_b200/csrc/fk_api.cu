@@ -106,6 +106,21 @@ PFN_addr_range addr_range_fn() {
   return g_addr_range.load();
 }
 
+// cuPointerGetAttributes, resolved the same way.
+typedef CUresult (*PFN_attributes)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
+
+PFN_attributes attributes_fn() {
+  static const PFN_attributes fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_attributes>(p);
+  }();
+  return fn;
+}
+
 // Is [p, p + bytes) memory the current device `dev` may access?
 fk_status check_pointer(const void* p, size_t bytes, int dev) {
   cudaPointerAttributes a;
@@ -183,6 +198,21 @@ fk_status validate_span(const void* p, size_t bytes, size_t align) {
   int dev = -1;
   const DeviceInfo* info = current_device_info(&dev);
   if (info == nullptr || !info->ok || info->major != 10 || info->minor != 0) return FK_ERR_UNSUPPORTED_DEVICE;
+  // device memory, the usual case, in one driver call; anything else through
+  // check_pointer
+  if (PFN_attributes f = attributes_fn()) {
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    unsigned type = 0;
+    int owner = -1;
+    CUpointer_attribute what[4] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                   CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+    void* into[4] = {&type, &owner, &base, &size};
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (f(4, what, into, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE &&
+        owner == dev && base != 0 && at >= base && at - base <= size && bytes <= size - (at - base))
+      return FK_OK;
+  }
   return check_pointer(p, bytes, dev);
 }
 

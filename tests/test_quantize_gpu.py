@@ -100,6 +100,32 @@ def test_special_rows(fk, torch_mod, cols, kind):
     assert np.all(c[5] == q8.QMAX[kind])
 
 
+@pytest.mark.parametrize("gelu", ["tanh", "erf"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [40, 64, 255, 1000, 2049, 4096, 9000, 16383, 16384, 40000])
+def test_gelu_of_special_rows(fk, torch_mod, cols, dtype, gelu):
+    """Rows whose largest magnitude is not at their largest value (all of them
+    negative or small), and rows with what is not finite: GELU(-inf) is -0, so
+    such a row keeps its scale."""
+    x = make_rows(12, cols, dtype, cols + 5)
+    x[0] = 0.0
+    x[1] = -x[1].abs() - 0.01                 # all negative
+    x[2] = -0.75                              # where GELU is lowest
+    x[3] = x[3].clamp(-0.7, 0.05)             # the dip outweighs the largest value
+    x[4] = -20.0                              # GELU vanishes
+    x[5, cols // 2] = float("nan")
+    x[6, cols - 1] = float("inf")
+    x[7, 0] = -float("inf")
+    x[8] = -x[8].abs()
+    x[8, cols // 3] = float("nan")            # a NaN among negative values
+    x[9] = x[9].clamp(-3.0, 0.17)
+    x[10, 0] = 1.0e30
+    for kind in ("i8", "e4m3"):
+        c, s = got = run(fk, torch_mod, x, kind, gelu)
+        check(x, kind, gelu, got)
+        assert np.isnan(s[[5, 6, 8]]).all() and np.isfinite(s[[0, 1, 2, 3, 4, 7, 9, 10]]).all()
+
+
 @pytest.mark.parametrize("kind", ["i8", "e4m3"])
 def test_every_code_and_ties(fk, torch_mod, kind):
     """Rows built to hit every code exactly, and every border between two:
