@@ -11,15 +11,13 @@
 // to the team's first threads, one each.  Inputs and outputs of the rows' type
 // then have to sit alike to 16 bytes; other buffers are streamed.
 //
-// Bound by HBM.  A thread holds 16 values (rows up to 4096 columns) or 32:
-// the loads of both inputs are all in flight before the first is used.
-// Blocks are as wide as the row needs, not the next power of two, so that
-// few lanes idle: 2560 columns take 160 threads.  Measured on B200 (64M
-// bf16 values, x + residual in, h and e4m3 codes out, L2 flushed, 2.6 us of
-// event overhead taken off): 4096 columns 6.08 TB/s at 16 values a thread,
-// 6.25 at 32 with 64 registers, 5.4 at 32 without a register limit, 4.8 at
-// 8; 8192 columns 5.63 / 5.92 / 5.12; 2048 columns 6.42 / 6.24 / 5.63; fp32
-// rows 6.1-6.6 at either.
+// Bound by HBM.  A thread holds four vectors (16 fp32 or 32 bf16 values): the
+// loads of both inputs are all in flight before the first is used, and 64
+// registers a thread keep 1024 threads on an SM.  Blocks are as wide as the
+// row needs, not the next power of two, so that few lanes idle: 2560 columns
+// take 96 threads of bf16.  Kernel arguments are __grid_constant__: copied to
+// the stack for the row's lambda, they cost 180 us against 158 (16384 x 4096
+// fp32, x + residual in, h and y out) and 108 against 81 (the same in bf16).
 #pragma once
 
 #include "fk_common.cuh"
@@ -32,7 +30,7 @@ namespace {
 constexpr int kRowWarps = 8;           // warps per block where a row takes a warp or less, at most
 constexpr int kRowLaneEpt = 8;         // values a thread where a row takes 8 or 16 lanes
 constexpr int kRowWarpCols = 1024;     // rows up to here take one warp
-constexpr int kRowBlockCols = 8192;    // up to here four vectors a thread
+constexpr int kRowBlockCols = 8192;    // RMSNorm: up to here four vectors a thread (fp32: 512 threads)
 constexpr int kRowLargeCols = 16384;   // up to here 32 values a thread, at most 512 threads
 constexpr int kRowMaxCols = 32768;     // the same, at most 1024 threads; longer rows are streamed
 constexpr size_t kRowMaxGrid = 0x7fffffffu;
@@ -88,9 +86,8 @@ __device__ __forceinline__ float round_one(float v) {
   return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-// Stores that stay where they are written in program order: left to itself
-// the compiler gathers a row's stores at its end, and 16384 x 4096 bf16 (x +
-// residual in, h and y out) goes from 94 us to 107.
+// Stores of a fixed width, write-back: the next operator of the chain reads
+// them, from L2 where they fit.
 __device__ __forceinline__ void st_v4(void* p, uint4 v) {
   asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }

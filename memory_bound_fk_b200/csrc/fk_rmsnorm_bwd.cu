@@ -1,8 +1,11 @@
 // fk_rmsnorm_bwd.cu -- gradients of the root-mean-square norm (sm_100a).
 //
 // With r = 1 / sqrt(sum h^2 / cols + eps) and s = sum dy gamma h / cols:
-//     dx_j     = r dy_j gamma_j - r^3 s h_j (+ dres_j),
+//     dx_j     = r dy_j gamma_j - r^3 s h_j (+ dres_j)
+//              = r (dy_j gamma_j - (r^2 s) h_j) (+ dres_j),
 //     dgamma_j = sum_rows dy_j h_j r.
+// The second form is what is computed: r^3 leaves fp32's range for rows of
+// about 1e-13 (with eps as small), r (r s) stays of the size of dy / h.
 // dgamma is summed in two steps whose order depends on the shape alone:
 // partial sums over groups of rows into workspace, then over the groups.
 #include <cuda_bf16.h>
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
       turn ^= 1;
     }
     const float r = rms_rstd(s, inv_n, a.eps);
-    const float r3s = r * r * r * (d * inv_n);
+    const float r2s = r * (r * (d * inv_n));
     if (!live) break;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         acc[c * VEC + k] = fmaf(g[k] * f[k], r, acc[c * VEC + k]);
-        o[k] = fmaf(r, g[k] * gam[c * VEC + k], -r3s * f[k]);
+        o[k] = r * fmaf(-r2s, f[k], g[k] * gam[c * VEC + k]);
       }
       if (a.dres) {
         float q[VEC];
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
     }
     if (!ALIGNED && edge >= 0) {
       ea = fmaf(ed * eh, r, ea);
-      Elem<T>::store1(static_cast<T*>(a.dx) + base + edge, fmaf(r, ed * eg, -r3s * eh) + er);
+      Elem<T>::store1(static_cast<T*>(a.dx) + base + edge, r * fmaf(-r2s, eh, ed * eg) + er);
       eh = neh;
       ed = ned;
     }
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
 
 // ---------------------------------------------------------------- streaming path
 
-// Row statistics: (r, r^3 s) of every row, one block per row.
+// Row statistics: (r, r^2 s) of every row, one block per row.
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads) rmsnorm_bwd_stats_kernel(RmsnormBwdArgs a, float2* stats) {
   __shared__ float2 red[kStreamThreads / 32];
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_bwd_stats_kernel(Rmsno
         d += red[w].y;
       }
       const float r = rms_rstd(s, inv_n, a.eps);
-      stats[row] = make_float2(r, r * r * r * (d * inv_n));
+      stats[row] = make_float2(r, r * (r * (d * inv_n)));
     }
     __syncthreads();  // red is rewritten by the next row
   }
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_bwd_dx_kernel(RmsnormB
       const float f = static_cast<float>(static_cast<const T*>(a.h)[i]);
       float g = static_cast<float>(static_cast<const T*>(a.dy)[i]);
       if (a.gamma) g *= a.gamma[j];
-      float v = fmaf(st.x, g, -st.y * f);
+      float v = st.x * fmaf(-st.y, f, g);
       if (a.dres) v += static_cast<float>(static_cast<const T*>(a.dres)[i]);
       static_cast<T*>(a.dx)[i] = static_cast<T>(v);
     }

@@ -364,3 +364,13 @@ def test_rows_behind_the_last_are_left(fk, torch_mod):
                               1e-6, s) == 0
     torch.cuda.synchronize()
     assert (out[6:] == 7).all() and (scales[6:] == 3).all() and (codes[6:] == 9).all() and EPS_HALF["f32"] == U
+
+
+@pytest.mark.parametrize("cols", [64, 1001, 4096, 12000, 40000])
+def test_backward_of_tiny_rows(fk, torch_mod, cols):
+    """Rows of about 1e-14 with eps = 0: r is about 1e14 and r^3 beyond fp32, the gradients are not."""
+    h = make_rows(5, cols, "f32", cols) * 1e-14
+    dy, g = make_rows(5, cols, "f32", cols + 1), gamma_of(cols, 3)
+    got = backward(fk, torch_mod, dy, h, g, None, True, 0.0)
+    assert np.isfinite(got[0]).all() and np.abs(got[0]).max() > 1e13
+    check_backward(dy, h, g, None, got, 0.0)
