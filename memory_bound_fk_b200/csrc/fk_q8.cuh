@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "fk_common.cuh"
+#include "fk_f32x2.cuh"
 #include "fk_q8.h"
 
 namespace fk {
@@ -46,8 +47,10 @@ struct Code8<FK_I8> {
     return __float_as_uint(fmaf(v, inv, 12582912.0f));
   }
   __device__ __forceinline__ static uint32_t pack4(const float* v, float inv) {
-    const uint32_t lo = __byte_perm(one(v[0], inv), one(v[1], inv), 0x0040);
-    const uint32_t hi = __byte_perm(one(v[2], inv), one(v[3], inv), 0x0040);
+    const float2 a = fma2(make_float2(v[0], v[1]), splat2(inv), splat2(12582912.0f));
+    const float2 b = fma2(make_float2(v[2], v[3]), splat2(inv), splat2(12582912.0f));
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
   }
   __device__ __forceinline__ static uint8_t pack1(float v, float inv) { return static_cast<uint8_t>(one(v, inv)); }
@@ -63,7 +66,8 @@ struct Code8<FK_E4M3> {
     return r;
   }
   __device__ __forceinline__ static uint32_t pack4(const float* v, float inv) {
-    return pair(v[0] * inv, v[1] * inv) | (static_cast<uint32_t>(pair(v[2] * inv, v[3] * inv)) << 16);
+    const float2 a = mul2(make_float2(v[0], v[1]), splat2(inv)), b = mul2(make_float2(v[2], v[3]), splat2(inv));
+    return pair(a.x, a.y) | (static_cast<uint32_t>(pair(b.x, b.y)) << 16);
   }
   __device__ __forceinline__ static uint8_t pack1(float v, float inv) {
     return static_cast<uint8_t>(pair(v * inv, 0.0f));

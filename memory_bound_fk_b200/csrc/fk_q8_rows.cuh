@@ -217,7 +217,8 @@ __device__ __forceinline__ void team_sum_max(float& s, float& m, float2* red) {
   }
 }
 
-// The maximum alone (of values: NaN if one is).
+// The maximum alone (of values: NaN if one is; at least 0 over a block).
+// `red`: 16-byte aligned, one word per warp, their number rounded up to four.
 template <int LANES>
 __device__ __forceinline__ void team_max(float& m, float* red) {
   auto larger = [](float a, float b) {
@@ -230,9 +231,13 @@ __device__ __forceinline__ void team_max(float& m, float* red) {
   if constexpr (LANES == 0) {
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    if (threadIdx.x < (-warps & 3)) red[warps + threadIdx.x] = 0.0f;
     __syncthreads();
-    m = red[0];
-    for (int w = 1; w < warps; ++w) m = larger(m, red[w]);
+    m = 0.0f;
+    for (int w = 0; w < warps; w += 4) {
+      const float4 z = *reinterpret_cast<const float4*>(red + w);
+      m = larger(m, larger(larger(z.x, z.y), larger(z.z, z.w)));
+    }
   }
 }
 

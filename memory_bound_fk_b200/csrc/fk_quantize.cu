@@ -43,19 +43,40 @@ __device__ __forceinline__ float2 act2(float2 x) {
   return x;
 }
 
-// A packed word's values raised to kActFloor (NaN stays), where GELU follows.
+// GELU of a pair with one reciprocal for both: 1 / s_x = s_y / (s_x s_y).
+// For values of at least kLowFloor, where the product stays in range.
+template <int EPI>
+__device__ __forceinline__ float2 act2_joint(float2 x) {
+  if constexpr (EPI == FK_EPILOGUE_GELU_TANH) {
+    const float2 a = mul2(x, fma2(splat2(kB), mul2(x, x), splat2(kA)));
+    const float2 s = add2(make_float2(ex2_ftz(a.y), ex2_ftz(a.x)), splat2(1.0f));  // the other's
+    return mul2(mul2(x, s), splat2(rcp_approx(s.x * s.y)));
+  }
+  if constexpr (EPI == FK_EPILOGUE_GELU_ERF) {
+    const float2 w = mul2(make_float2(fabsf(x.x), fabsf(x.y)), splat2(kRsqrt2));
+    const float2 s = fma2(splat2(0.5f), make_float2(w.y, w.x), splat2(1.0f));
+    const float2 t = mul2(s, splat2(rcp_approx(s.x * s.y)));
+    const float2 e = mul2(fma2(make_float2(-w.x, -w.y), w, erfc_poly(t)), splat2(kLog2e));
+    const float2 h = mul2(mul2(splat2(0.5f), t), make_float2(ex2_ftz(e.x), ex2_ftz(e.y)));
+    const float2 sg = make_float2(phi_sign(x.x), phi_sign(x.y));
+    return mul2(x, fma2(sg, h, fma2(sg, splat2(-0.5f), splat2(0.5f))));
+  }
+  return x;
+}
+
+// A packed word's values raised to a floor (NaN stays), where GELU follows.
 template <typename T, int EPI>
-__device__ __forceinline__ uint4 raised(uint4 w) {
+__device__ __forceinline__ uint4 raised(uint4 w, float floor = kActFloor, uint32_t floor_pair = kActFloorPair) {
   if constexpr (EPI != FK_EPILOGUE_NONE && sizeof(T) == 4) {
-    w.x = __float_as_uint(max_nan(__uint_as_float(w.x), kActFloor));
-    w.y = __float_as_uint(max_nan(__uint_as_float(w.y), kActFloor));
-    w.z = __float_as_uint(max_nan(__uint_as_float(w.z), kActFloor));
-    w.w = __float_as_uint(max_nan(__uint_as_float(w.w), kActFloor));
+    w.x = __float_as_uint(max_nan(__uint_as_float(w.x), floor));
+    w.y = __float_as_uint(max_nan(__uint_as_float(w.y), floor));
+    w.z = __float_as_uint(max_nan(__uint_as_float(w.z), floor));
+    w.w = __float_as_uint(max_nan(__uint_as_float(w.w), floor));
   } else if constexpr (EPI != FK_EPILOGUE_NONE) {
-    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(kActFloorPair));
-    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(kActFloorPair));
-    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.z) : "r"(kActFloorPair));
-    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w) : "r"(kActFloorPair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(floor_pair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(floor_pair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.z) : "r"(floor_pair));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w) : "r"(floor_pair));
   }
   return w;
 }
@@ -68,6 +89,12 @@ __device__ __forceinline__ float act(float x) {
 // from there on: where GELU of a row's largest value is above this, it is the
 // row's largest magnitude, and no other value's GELU is needed for the scale.
 constexpr float kGeluDip = 0.1725f;
+// In such a row every value below this has the code 0 (|GELU| there is under
+// 4e-13, the smallest scale 0.1725 / 448): values are raised to it, which
+// bounds what two of them exponentiate together (2^61 each, tanh form).
+// Exact in bf16.
+constexpr float kLowFloor = -7.5f;
+constexpr uint32_t kLowFloorPair = 0xc0f0c0f0u;
 
 // Largest value (not magnitude) among m and a vector's, NaN if one is.
 template <typename T>
@@ -89,7 +116,7 @@ __device__ __forceinline__ float max_words(float m, const uint4& w) {
 template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_constant__ QuantizeArgs a) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  __shared__ float red[LANES ? 1 : MAXT / 32];
+  __shared__ __align__(16) float red[LANES ? 1 : MAXT / 32];
   let_next_start();
   after_previous();
   for_rows<LANES>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
@@ -128,37 +155,32 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_c
   });
 }
 
-// Wide rows: blocks that stay and walk the rows, the next row loaded before
-// the current one is computed.
-template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int MAXT, int MINB>
+// Wide bf16 rows: blocks that stay and walk the rows, the next row loaded
+// before the current one is computed.  Measured on B200 (8192 x 16384 to
+// e4m3): 63 us plain (6.4 TB/s), 80 through the tanh form (93 with a
+// reciprocal for each value, one read a warp of the row's maxima and the
+// scale applied to single values), 137 through the erf form (25 instructions
+// a value: issue).  The tanh form's rest: MUFU, with 1.5 operations a value
+// at least 46 us, and issue, at 15 instructions a value 57, in turns between
+// barriers.
+// Rows of up to 8192 columns do not gain (4096: 38.4 against 37.5 with one
+// row per block), nor do shifted ones (16383: 112 against 96).
+template <typename T, int OUT, int EPI, int EPT, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_constant__ QuantizeArgs a) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  __shared__ float red[2][MAXT / 32], dip[MAXT / 32];
+  __shared__ __align__(16) float red[2][MAXT / 32], dip[MAXT / 32];
   const int cols = static_cast<int>(a.cols), t = static_cast<int>(threadIdx.x), team = static_cast<int>(blockDim.x);
   const T* const x = static_cast<const T*>(a.x);
   let_next_start();
   after_previous();
   uint4 raw[VPT];
-  float ev = 0.0f;
-  if (blockIdx.x < a.rows) {
-    const T* const first = x + blockIdx.x * a.cols;
-    const Place p = place_of<T, ALIGNED>(t, team, cols, first);
-    load_vecs<T, VPT>(first, p, raw);
-    if (!ALIGNED && edge_col<VEC>(p) >= 0) ev = load_one(first + edge_col<VEC>(p));
-  }
+  const Place p = place_of<T, true>(t, team, cols, x);
+  if (blockIdx.x < a.rows) load_vecs<T, VPT>(x + blockIdx.x * a.cols, p, raw);
   int turn = 0;
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const size_t base = row * a.cols;
-    const Place p = place_of<T, ALIGNED>(t, team, cols, x + base);
-    const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
     uint4 next[VPT];
-    float nev = 0.0f;
-    if (row + gridDim.x < a.rows) {
-      const T* const nx = x + base + gridDim.x * a.cols;
-      const Place np = place_of<T, ALIGNED>(t, team, cols, nx);
-      load_vecs<T, VPT>(nx, np, next);
-      if (!ALIGNED && edge_col<VEC>(np) >= 0) nev = load_one(nx + edge_col<VEC>(np));
-    }
+    if (row + gridDim.x < a.rows) load_vecs<T, VPT>(x + base + gridDim.x * a.cols, p, next);
     // the row's largest magnitude: for GELU, from its largest value alone
     // where that decides, so that the values stay packed until their codes
     // are made
@@ -174,12 +196,12 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_
         m = max_words<T>(m, raw[c]);
       }
     }
-    if (!ALIGNED && edge >= 0) m = EPI == FK_EPILOGUE_NONE ? absmax_nan(m, ev) : max_nan(m, ev);
     team_max<0>(m, red[turn]);
+    bool rises = false;
     if constexpr (EPI != FK_EPILOGUE_NONE) {
       m = act<EPI>(m);
-      ev = act<EPI>(ev);
-      if (!(m > kGeluDip)) {  // small or negative values only, or a NaN: the same for the whole block
+      rises = m > kGeluDip;
+      if (!rises) {  // small or negative values only, or a NaN: the same for the whole block
         m = 0.0f;
 #pragma unroll 1
         for (int j = t; j < cols; j += team) m = absmax_nan(m, act<EPI>(static_cast<float>(x[base + j])));
@@ -191,21 +213,35 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_
     const RowScale q = row_scale<OUT>(m);
     uint8_t* const o = static_cast<uint8_t*>(a.q) + base;
     if (t == 0) a.scales[row] = q.scale;
+    if (rises) {
 #pragma unroll
-    for (int c = 0; c < VPT; ++c) {
-      float f[VEC];
-      Elem<T>::unpack(raised<T, EPI>(raw[c]), f);
+      for (int c = 0; c < VPT; ++c) {
+        float f[VEC];
+        Elem<T>::unpack(raised<T, EPI>(raw[c], kLowFloor, kLowFloorPair), f);
 #pragma unroll
-      for (int k = 0; k < VEC; k += 2) {
-        const float2 z = act2<EPI>(make_float2(f[k], f[k + 1]));
-        f[k] = z.x;
-        f[k + 1] = z.y;
+        for (int k = 0; k < VEC; k += 2) {
+          const float2 z = act2_joint<EPI>(make_float2(f[k], f[k + 1]));
+          f[k] = z.x;
+          f[k + 1] = z.y;
+        }
+        store_codes<T, OUT, true>(o, p, c, f, q);
       }
-      store_codes<T, OUT, ALIGNED>(o, p, c, f, q);
-      raw[c] = next[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < VPT; ++c) {
+        float f[VEC];
+        Elem<T>::unpack(raised<T, EPI>(raw[c]), f);
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+          const float2 z = act2<EPI>(make_float2(f[k], f[k + 1]));
+          f[k] = z.x;
+          f[k + 1] = z.y;
+        }
+        store_codes<T, OUT, true>(o, p, c, f, q);
+      }
     }
-    if (!ALIGNED && edge >= 0) o[edge] = q.ok ? Code8<OUT>::pack1(ev, q.inv) : 0;
-    ev = nev;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) raw[c] = next[c];
   }
 }
 
@@ -249,11 +285,13 @@ cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 32, 32 * kRowWarps, 4>, l.grid, l.threads, 0, 1, s, a);
   }
   const RowLaunch l = block_launch(a.rows, a.cols, 32);
-  if (sizeof(T) == 2 && a.cols > kRowBlockCols && a.cols <= kRowLargeCols) {
-    // as many blocks as stay resident: 1024 threads an SM at 64 registers
-    const unsigned fit = 148u * (1024u / l.threads);
-    return launch_overlapped(quantize_walk_kernel<T, OUT, EPI, 32, ALIGNED, 512, 2>, l.grid < fit ? l.grid : fit,
-                             l.threads, 0, 1, s, a);
+  if constexpr (sizeof(T) == 2 && ALIGNED) {
+    if (a.cols > kRowBlockCols && a.cols <= kRowLargeCols) {
+      // as many blocks as stay resident: 1024 threads an SM at 64 registers
+      const unsigned fit = 148u * (1024u / l.threads);
+      return launch_overlapped(quantize_walk_kernel<T, OUT, EPI, 32, 512, 2>, l.grid < fit ? l.grid : fit,
+                               l.threads, 0, 1, s, a);
+    }
   }
   if (a.cols <= kRowLargeCols)
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
