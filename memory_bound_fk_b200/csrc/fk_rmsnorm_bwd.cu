@@ -50,33 +50,30 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 // 8 values a thread 5.61.  8192 columns (one 512-thread block per SM) 5.86.
 // 16384 columns in one block: 3.4 TB/s at 32 values a thread, 3.0 with 1024
 // threads, hence the clusters.
-template <typename T, int EPT, bool ALIGNED, int LANES, int CL, int MAXT>
+template <typename T, int EPT, bool ALIGNED, int LANES, int MAXT>
 __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 ? 2 : small_blocks(Elem<T>::VEC)) rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   constexpr bool WARP = LANES > 0;
   constexpr int PER = WARP ? 32 / (WARP ? LANES : 1) : 1;  // rows a warp takes at a time
-  constexpr int TEAMS = CL > 1 ? CL : 1;
   // two scratch rows in turn, one pair per warp of the team: one barrier a row
-  __shared__ float2 red[2][WARP ? 1 : TEAMS * (MAXT / 32)];
+  __shared__ float2 red[2][WARP ? 1 : MAXT / 32];
   const int cols = static_cast<int>(a.cols);
   const float inv_n = 1.0f / static_cast<float>(cols);
   const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
-  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int lane = static_cast<int>(threadIdx.x & 31);
   const size_t team = WARP ? (static_cast<size_t>(blockIdx.x) * warps + warp) * PER + lane / (WARP ? LANES : 32)
-                           : blockIdx.x / TEAMS;
-  const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps * PER : gridDim.x / TEAMS;
+                           : blockIdx.x;
+  const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps * PER : gridDim.x;
   const T* const h = static_cast<const T*>(a.h);
   const T* const dy = static_cast<const T*>(a.dy);
   const T* const dres = static_cast<const T*>(a.dres);
   // shifted rows: a team's rows are a multiple of eight apart (or it has one),
   // so that all of them start alike
-  const Place p = place_of<T, ALIGNED>(WARP ? lane % (WARP ? LANES : 32) : static_cast<int>(rank * blockDim.x + threadIdx.x),
-                                       WARP ? LANES : static_cast<int>(TEAMS * blockDim.x), cols, h + team * a.cols);
+  const Place p = place_of<T, ALIGNED>(WARP ? lane % (WARP ? LANES : 32) : static_cast<int>(threadIdx.x),
+                                       WARP ? LANES : static_cast<int>(blockDim.x), cols, h + team * a.cols);
   const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
   let_next_start();
   after_previous();
-  if constexpr (CL > 1) cluster_arrive_relaxed();  // every block has started: waited for before the first push
   float gam[EPT], acc[EPT];
   float eg = 1.0f, ea = 0.0f, eh = 0.0f, ed = 0.0f;  // gamma, sum, h and dy of this thread's column outside the vectors
   if (!ALIGNED && edge >= 0 && a.gamma) eg = __ldg(a.gamma + edge);
@@ -95,7 +92,6 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
       ed = load_one(dy + team * a.cols + edge);
     }
   }
-  if constexpr (CL > 1) cluster_wait();
   int turn = 0;
   // (a warp's teams go on together until the last of them has no row left)
   for (size_t row = team; row - lane / (WARP ? LANES : 32) < a.rows; row += stride) {
@@ -137,16 +133,11 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
       d += __shfl_xor_sync(0xffffffffu, d, o);
     }
     if constexpr (!WARP) {
-      if constexpr (CL > 1) {
-        if (lane < TEAMS) st_cluster_f2(cluster_addr(&red[turn][rank * warps + warp], lane), s, d);
-        cluster_barrier();
-      } else {
-        if (lane == 0) red[turn][warp] = make_float2(s, d);
-        __syncthreads();
-      }
+      if (lane == 0) red[turn][warp] = make_float2(s, d);
+      __syncthreads();
       s = red[turn][0].x;
       d = red[turn][0].y;
-      for (int w = 1; w < TEAMS * warps; ++w) {
+      for (int w = 1; w < warps; ++w) {
         s += red[turn][w].x;
         d += red[turn][w].y;
       }
@@ -183,7 +174,7 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
     }
   }
   if (partial == nullptr) return;
-  float* out = partial + static_cast<size_t>(blockIdx.x / TEAMS) * a.cols;
+  float* out = partial + static_cast<size_t>(blockIdx.x) * a.cols;
   __shared__ float sums[WARP ? MAXT / 32 * PER : 1][WARP ? LANES * EPT : 1];
   float* const mine = WARP ? sums[threadIdx.x / (WARP ? LANES : 1)] : out;
 #pragma unroll
@@ -200,6 +191,166 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
       out[e] = v;
     }
   }
+}
+
+// ---------------------------------------------------------------- rows staged in shared memory
+
+// 16 bytes from global to shared memory without registers; zeros when !on
+// (nothing is read then).
+__device__ __forceinline__ void copy16_async(uint4* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last committed group of this thread's copies have landed (or all).
+__device__ __forceinline__ void copies_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+constexpr int kStageVecs = 4;  // 16-byte vectors a thread holds of a row in each buffer
+
+// Blocks that stay and walk the rows, as above, for rows longer than a
+// block's registers: a row's h, dy and dres wait in shared memory, two rows
+// at a time.  A thread fills and reads only its own slots (copies that pass
+// the registers by, two rows ahead), so the one barrier of a row is that of
+// its sums.  CL blocks of a cluster share a row.
+template <typename T, bool ALIGNED, int CL>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    rmsnorm_bwd_staged_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
+  constexpr int VEC = Elem<T>::VEC, VPT = kStageVecs, EPT = VEC * VPT;
+  extern __shared__ uint4 slots[];  // [2 rows][h, dy (, dres)][vector][thread]
+  __shared__ float2 red[2][CL * (kBwdThreads / 32)];
+  const int cols = static_cast<int>(a.cols);
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const size_t team = blockIdx.x / CL, stride = gridDim.x / CL;
+  const T* const h = static_cast<const T*>(a.h);
+  const T* const dy = static_cast<const T*>(a.dy);
+  const T* const dres = static_cast<const T*>(a.dres);
+  const int bufs = dres ? 3 : 2;
+  // shifted rows: a team's rows are a multiple of eight apart (or it has one),
+  // so that all of them start alike
+  const Place p = place_of<T, ALIGNED>(static_cast<int>(rank * blockDim.x + threadIdx.x),
+                                       static_cast<int>(CL * blockDim.x), cols, h + team * a.cols);
+  const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
+  auto slot = [&](int st, int buf, int c) {
+    return slots + ((st * bufs + buf) * VPT + c) * static_cast<int>(blockDim.x) + threadIdx.x;
+  };
+  auto fetch = [&](int st, size_t row, int c) {
+    const bool on = row < a.rows && has_vec(p, c);
+    const size_t at = on ? row * a.cols + col_of_vec<VEC>(p, c) : 0;
+    copy16_async(slot(st, 0, c), h + at, on);
+    copy16_async(slot(st, 1, c), dy + at, on);
+    if (dres) copy16_async(slot(st, 2, c), dres + at, on);
+  };
+  let_next_start();
+  after_previous();
+  if constexpr (CL > 1) cluster_arrive_relaxed();  // every block has started: waited for before the first push
+#pragma unroll
+  for (int st = 0; st < 2; ++st) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) fetch(st, team + st * stride, c);
+    copies_commit();
+  }
+  float gam[EPT], acc[EPT];
+  float eg = 1.0f, ea = 0.0f, eh = 0.0f, ed = 0.0f;  // gamma, sum, h and dy of this thread's column outside the vectors
+  if (!ALIGNED && edge >= 0) {
+    if (a.gamma) eg = __ldg(a.gamma + edge);
+    if (team < a.rows) {
+      eh = load_one(h + team * a.cols + edge);
+      ed = load_one(dy + team * a.cols + edge);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < VPT; ++c) load_params<VEC, ALIGNED>(a.gamma, p, c, gam + c * VEC);
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) acc[i] = 0.0f;
+  if constexpr (CL > 1) cluster_wait();
+  int st = 0;
+  for (size_t row = team; row < a.rows; row += stride, st ^= 1) {
+    const size_t base = row * a.cols, next = base + stride * a.cols;
+    float neh = 0.0f, ned = 0.0f, er = 0.0f;
+    if (!ALIGNED && edge >= 0) {
+      if (dres) er = load_one(dres + base + edge);
+      if (row + stride < a.rows) {
+        neh = load_one(h + next + edge);
+        ned = load_one(dy + next + edge);
+      }
+    }
+    copies_wait_but_one();
+    float s = 0.0f, d = 0.0f;
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float f[VEC], g[VEC];
+      Elem<T>::unpack(*slot(st, 0, c), f);
+      Elem<T>::unpack(*slot(st, 1, c), g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        s = fmaf(f[k], f[k], s);
+        d = fmaf(g[k] * gam[c * VEC + k], f[k], d);
+      }
+    }
+    if (!ALIGNED && edge >= 0) {
+      s = fmaf(eh, eh, s);
+      d = fmaf(ed * eg, eh, d);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      d += __shfl_xor_sync(0xffffffffu, d, o);
+    }
+    if constexpr (CL > 1) {
+      if (lane < CL) st_cluster_f2(cluster_addr(&red[st][rank * warps + warp], lane), s, d);
+      cluster_barrier();
+    } else {
+      if (lane == 0) red[st][warp] = make_float2(s, d);
+      __syncthreads();
+    }
+    s = red[st][0].x;
+    d = red[st][0].y;
+    for (int w = 1; w < CL * warps; ++w) {
+      s += red[st][w].x;
+      d += red[st][w].y;
+    }
+    const float r = rms_rstd(s, inv_n, a.eps);
+    const float r2s = r * (r * (d * inv_n));
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float f[VEC], g[VEC], o[VEC];
+      Elem<T>::unpack(*slot(st, 0, c), f);
+      Elem<T>::unpack(*slot(st, 1, c), g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        acc[c * VEC + k] = fmaf(g[k] * f[k], r, acc[c * VEC + k]);
+        o[k] = r * fmaf(-r2s, f[k], g[k] * gam[c * VEC + k]);
+      }
+      if (dres) {
+        float q[VEC];
+        Elem<T>::unpack(*slot(st, 2, c), q);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] += q[k];
+      }
+      store_vec(static_cast<T*>(a.dx) + base, p, c, Elem<T>::pack(o));
+      fetch(st, row + 2 * stride, c);  // the slots have been read: what was stored came from them
+    }
+    copies_commit();
+    if (!ALIGNED && edge >= 0) {
+      ea = fmaf(ed * eh, r, ea);
+      Elem<T>::store1(static_cast<T*>(a.dx) + base + edge, r * fmaf(-r2s, eh, ed * eg) + er);
+      eh = neh;
+      ed = ned;
+    }
+  }
+  copies_wait();
+  if (partial == nullptr) return;
+  float* const out = partial + team * a.cols;
+#pragma unroll
+  for (int c = 0; c < VPT; ++c)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (has_vec(p, c)) out[col_of_vec<VEC>(p, c) + k] = acc[c * VEC + k];
+  if (!ALIGNED && edge >= 0) out[edge] = ea;
 }
 
 // ---------------------------------------------------------------- streaming path
@@ -328,7 +479,7 @@ cudaError_t launch_stream(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 // How the registers-resident kernel is launched for a shape: blocks, threads,
 // blocks per team, rows of partial sums.
 struct BwdLaunch {
-  int lanes, ept, cluster, threads;
+  int lanes, ept, cluster, threads;  // cluster: 0 for warp teams
   size_t blocks, groups;
 };
 
@@ -348,20 +499,35 @@ BwdLaunch bwd_launch(size_t rows, size_t cols, int vec, bool shifted) {
     return l;
   }
   l.lanes = 0;
-  l.ept = kBwdEpt;
-  l.cluster = cols <= kBwdBlockCols ? 1 : cols <= 2 * kBwdBlockCols ? 2 : 4;
-  const size_t per = kBwdEpt * static_cast<size_t>(l.cluster);
+  l.cluster = 1;
+  if (cols <= kBwdBlockCols) {
+    l.ept = kBwdEpt;
+  } else {
+    l.ept = kStageVecs * vec;
+    while (l.cluster * kBwdThreads * l.ept < static_cast<int>(cols)) l.cluster *= 2;
+  }
+  const size_t per = static_cast<size_t>(l.ept) * l.cluster;
   l.threads = static_cast<int>(((cols + per - 1) / per + 31) / 32 * 32);
-  const size_t fit = kSmCount / l.cluster * (l.cluster == 1 ? kBwdThreads / l.threads : 1);
+  const size_t fit = kSmCount / l.cluster * (cols <= kBwdBlockCols ? kBwdThreads / l.threads : 1);
   l.groups = rows < fit ? rows : shifted ? fit / 8 * 8 : fit;
   l.blocks = l.groups * l.cluster;
   return l;
 }
 
-template <typename T, int EPT, bool ALIGNED, int LANES, int CL, int MAXT>
+template <typename T, int EPT, bool ALIGNED, int LANES, int MAXT>
 cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, LANES, CL, MAXT>,
-                           static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), 0, CL > 1 ? CL : 1, s, a,
+  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, LANES, MAXT>, static_cast<unsigned>(l.blocks),
+                           static_cast<unsigned>(l.threads), 0, 1, s, a, partial);
+}
+
+template <typename T, bool ALIGNED, int CL>
+cudaError_t launch_staged_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
+  auto kernel = rmsnorm_bwd_staged_kernel<T, ALIGNED, CL>;
+  const size_t smem = size_t{2} * (a.dres ? 3 : 2) * kStageVecs * 16 * l.threads;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kernel, static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), smem, CL, s, a,
                            partial);
 }
 
@@ -371,15 +537,16 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
   float* partial = a.dgamma ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaErrorInvalidValue;
   if (l.lanes > 0) {
-    if (l.lanes == 8) e = launch_row_kernel<T, 8, ALIGNED, 8, 1, 256>(a, partial, l, s);
-    if (l.lanes == 16) e = launch_row_kernel<T, 8, ALIGNED, 16, 1, 256>(a, partial, l, s);
-    if (l.lanes == 32 && l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 32, 1, 256>(a, partial, l, s);
-    if (l.lanes == 32 && l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 32, 1, 256>(a, partial, l, s);
-    if (l.lanes == 32 && l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 32, 1, 256>(a, partial, l, s);
+    if (l.lanes == 8) e = launch_row_kernel<T, 8, ALIGNED, 8, 256>(a, partial, l, s);
+    if (l.lanes == 16) e = launch_row_kernel<T, 8, ALIGNED, 16, 256>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 32, 256>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 32, 256>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 32, 256>(a, partial, l, s);
   } else {
-    if (l.cluster == 1) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, 1, kBwdThreads>(a, partial, l, s);
-    if (l.cluster == 2) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, 2, kBwdThreads>(a, partial, l, s);
-    if (l.cluster == 4) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, 4, kBwdThreads>(a, partial, l, s);
+    if (a.cols <= kBwdBlockCols) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, kBwdThreads>(a, partial, l, s);
+    else if (l.cluster == 1) e = launch_staged_kernel<T, ALIGNED, 1>(a, partial, l, s);
+    else if (l.cluster == 2) e = launch_staged_kernel<T, ALIGNED, 2>(a, partial, l, s);
+    else if (l.cluster == 4) e = launch_staged_kernel<T, ALIGNED, 4>(a, partial, l, s);
   }
   if (e != cudaSuccess || partial == nullptr) return e;
   return launch_join(partial, a.dgamma, a.cols, l.groups, s);
