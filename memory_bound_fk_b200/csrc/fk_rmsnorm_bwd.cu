@@ -23,9 +23,7 @@ constexpr int kStreamThreads = 512;
 constexpr size_t kMaxGrid = 0x7fffffffu;
 constexpr int kColThreads = 128;      // columns per block of the column sums
 constexpr int kJoinCols = 32, kJoinWays = 32;
-constexpr int kBwdEpt = 16;           // values a thread holds of a row (8 or 32 in a warp team where that fits better)
-constexpr int kBwdThreads = 512;
-constexpr size_t kBwdBlockCols = kBwdEpt * kBwdThreads;  // columns a block holds
+constexpr int kBwdThreads = 512;      // of a block whose rows are staged, at most
 // Blocks per SM of warp teams with 8 values a lane (registers follow): 200000 x
 // 64 fp32 29 us at three and 35 at four, 100000 x 128 bf16 27 and 25.
 constexpr int small_blocks(int vec) { return vec == 8 ? 4 : 3; }
@@ -34,43 +32,29 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 
 // ---------------------------------------------------------------- rows held in registers
 
-// Blocks that stay on the GPU and walk the rows.  The team of a row is LANES
-// lanes of a warp (up to 1024 columns), or (LANES = 0) the CL blocks of a
-// cluster (one up to 8192 columns), so that a thread's columns never change: gamma and the running
-// dgamma sums live in its registers.  The next row's h and dy are loaded
-// before the current one is reduced, which keeps HBM busy through the
-// reduction.  At the end each block writes its columns' partial sums, one row
-// of workspace per team block (the warps of a warp-team block added first, in
-// order).
-//
-// Bound by HBM.  16 values a thread and as many registers as they take (two
-// 256-thread blocks per SM).  Measured on B200 (64M bf16 values, four streams
-// of them, event overhead taken off): 4096 columns 5.99 TB/s; without the
-// prefetch 4.79; with registers capped for three blocks per SM 4.18 (spills);
-// 8 values a thread 5.61.  8192 columns (one 512-thread block per SM) 5.86.
-// 16384 columns in one block: 3.4 TB/s at 32 values a thread, 3.0 with 1024
-// threads, hence the clusters.
-template <typename T, int EPT, bool ALIGNED, int LANES, int MAXT>
-__global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 ? 2 : small_blocks(Elem<T>::VEC)) rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
+// Rows of up to 1024 columns: blocks that stay on the GPU and walk the rows,
+// LANES lanes of a warp to a row, so that a thread's columns never change:
+// gamma and the running dgamma sums live in its registers.  The next row's h
+// and dy are loaded before the current one is reduced, which keeps HBM busy
+// through the reduction.  At the end each block adds its warps' sums in order
+// and writes them, one row of workspace per block.
+template <typename T, int EPT, bool ALIGNED, int LANES>
+__global__ void __launch_bounds__(32 * kRowWarps, EPT == 32 ? 1 : EPT == 16 ? 2 : small_blocks(Elem<T>::VEC))
+    rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  constexpr bool WARP = LANES > 0;
-  constexpr int PER = WARP ? 32 / (WARP ? LANES : 1) : 1;  // rows a warp takes at a time
-  // two scratch rows in turn, one pair per warp of the team: one barrier a row
-  __shared__ float2 red[2][WARP ? 1 : MAXT / 32];
+  constexpr int PER = 32 / LANES;  // rows a warp takes at a time
   const int cols = static_cast<int>(a.cols);
   const float inv_n = 1.0f / static_cast<float>(cols);
   const int warps = static_cast<int>(blockDim.x >> 5), warp = static_cast<int>(threadIdx.x >> 5);
   const int lane = static_cast<int>(threadIdx.x & 31);
-  const size_t team = WARP ? (static_cast<size_t>(blockIdx.x) * warps + warp) * PER + lane / (WARP ? LANES : 32)
-                           : blockIdx.x;
-  const size_t stride = WARP ? static_cast<size_t>(gridDim.x) * warps * PER : gridDim.x;
+  const size_t team = (static_cast<size_t>(blockIdx.x) * warps + warp) * PER + lane / LANES;
+  const size_t stride = static_cast<size_t>(gridDim.x) * warps * PER;
   const T* const h = static_cast<const T*>(a.h);
   const T* const dy = static_cast<const T*>(a.dy);
   const T* const dres = static_cast<const T*>(a.dres);
   // shifted rows: a team's rows are a multiple of eight apart (or it has one),
   // so that all of them start alike
-  const Place p = place_of<T, ALIGNED>(WARP ? lane % (WARP ? LANES : 32) : static_cast<int>(threadIdx.x),
-                                       WARP ? LANES : static_cast<int>(blockDim.x), cols, h + team * a.cols);
+  const Place p = place_of<T, ALIGNED>(lane % LANES, LANES, cols, h + team * a.cols);
   const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
   let_next_start();
   after_previous();
@@ -92,11 +76,10 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
       ed = load_one(dy + team * a.cols + edge);
     }
   }
-  int turn = 0;
   // (a warp's teams go on together until the last of them has no row left)
-  for (size_t row = team; row - lane / (WARP ? LANES : 32) < a.rows; row += stride) {
+  for (size_t row = team; row - lane / LANES < a.rows; row += stride) {
     const size_t base = row * a.cols, next = base + stride * a.cols;
-    const bool live = !WARP || row < a.rows;
+    const bool live = row < a.rows;
     uint4 nh[VPT], nd[VPT], rr[VPT];
     float neh = 0.0f, ned = 0.0f, er = 0.0f;
     if (a.dres && live) {
@@ -128,20 +111,9 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
       d = fmaf(ed * eg, eh, d);
     }
 #pragma unroll
-    for (int o = (WARP ? LANES : 32) / 2; o > 0; o >>= 1) {
+    for (int o = LANES / 2; o > 0; o >>= 1) {
       s += __shfl_xor_sync(0xffffffffu, s, o);
       d += __shfl_xor_sync(0xffffffffu, d, o);
-    }
-    if constexpr (!WARP) {
-      if (lane == 0) red[turn][warp] = make_float2(s, d);
-      __syncthreads();
-      s = red[turn][0].x;
-      d = red[turn][0].y;
-      for (int w = 1; w < warps; ++w) {
-        s += red[turn][w].x;
-        d += red[turn][w].y;
-      }
-      turn ^= 1;
     }
     const float r = rms_rstd(s, inv_n, a.eps);
     const float r2s = r * (r * (d * inv_n));
@@ -175,48 +147,59 @@ __global__ void __launch_bounds__(MAXT, LANES == 0 || EPT == 32 ? 1 : EPT == 16 
   }
   if (partial == nullptr) return;
   float* out = partial + static_cast<size_t>(blockIdx.x) * a.cols;
-  __shared__ float sums[WARP ? MAXT / 32 * PER : 1][WARP ? LANES * EPT : 1];
-  float* const mine = WARP ? sums[threadIdx.x / (WARP ? LANES : 1)] : out;
+  __shared__ float sums[kRowWarps * PER][LANES * EPT];
+  float* const mine = sums[threadIdx.x / LANES];
 #pragma unroll
   for (int c = 0; c < VPT; ++c)
 #pragma unroll
     for (int k = 0; k < VEC; ++k)
       if (has_vec(p, c)) mine[col_of_vec<VEC>(p, c) + k] = acc[c * VEC + k];
   if (!ALIGNED && edge >= 0) mine[edge] = ea;
-  if constexpr (WARP) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < cols; e += blockDim.x) {
-      float v = sums[0][e];
-      for (int w = 1; w < warps * PER; ++w) v += sums[w][e];
-      out[e] = v;
-    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < cols; e += blockDim.x) {
+    float v = sums[0][e];
+    for (int w = 1; w < warps * PER; ++w) v += sums[w][e];
+    out[e] = v;
   }
 }
 
 // ---------------------------------------------------------------- rows staged in shared memory
 
-// 16 bytes from global to shared memory without registers; zeros when !on
-// (nothing is read then).
+// 16 bytes from global to shared memory without registers (past L1 where
+// ALIGNED); zeros when !on (nothing is read then).
+template <bool ALIGNED>
 __device__ __forceinline__ void copy16_async(uint4* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
-               : "memory");
+  if constexpr (ALIGNED)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the last committed group of this thread's copies have landed (or all).
 __device__ __forceinline__ void copies_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-constexpr int kStageVecs = 4;  // 16-byte vectors a thread holds of a row in each buffer
 
-// Blocks that stay and walk the rows, as above, for rows longer than a
-// block's registers: a row's h, dy and dres wait in shared memory, two rows
-// at a time.  A thread fills and reads only its own slots (copies that pass
-// the registers by, two rows ahead), so the one barrier of a row is that of
-// its sums.  CL blocks of a cluster share a row.
-template <typename T, bool ALIGNED, int CL>
+// Longer rows: blocks that stay and walk the rows, as above, a row's h, dy
+// and dres waiting in shared memory, two rows at a time.  A thread fills and
+// reads only its own slots (copies that pass the registers by, two rows
+// ahead), so the one barrier of a row is that of its sums.  CL blocks of a
+// cluster share a row.
+//
+// Bound by HBM.  Measured on B200 (64M values, h, dy and dres in, dx out,
+// event overhead and the second step of dgamma included): bf16 4096 columns
+// 85.5 us (6.3 TB/s; with the next row prefetched into registers instead
+// 90.5), 8192 columns 90 (93), 16384 columns 100 (147, two blocks of a
+// cluster); fp32 64M values of 8192 columns 167 (191: spills).  Shifted rows
+// copy through L1 (.ca): past it, the boundaries between lanes' 16 bytes
+// that are no sector boundaries are read twice (8191 columns fp32: 194 us
+// against 207); bf16 4095 columns 112, 16383 146.
+template <typename T, int EPT, bool ALIGNED, int CL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     rmsnorm_bwd_staged_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
-  constexpr int VEC = Elem<T>::VEC, VPT = kStageVecs, EPT = VEC * VPT;
+  constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   extern __shared__ uint4 slots[];  // [2 rows][h, dy (, dres)][vector][thread]
   __shared__ float2 red[2][CL * (kBwdThreads / 32)];
   const int cols = static_cast<int>(a.cols);
@@ -240,9 +223,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   auto fetch = [&](int st, size_t row, int c) {
     const bool on = row < a.rows && has_vec(p, c);
     const size_t at = on ? row * a.cols + col_of_vec<VEC>(p, c) : 0;
-    copy16_async(slot(st, 0, c), h + at, on);
-    copy16_async(slot(st, 1, c), dy + at, on);
-    if (dres) copy16_async(slot(st, 2, c), dres + at, on);
+    copy16_async<ALIGNED>(slot(st, 0, c), h + at, on);
+    copy16_async<ALIGNED>(slot(st, 1, c), dy + at, on);
+    if (dres) copy16_async<ALIGNED>(slot(st, 2, c), dres + at, on);
   };
   let_next_start();
   after_previous();
@@ -483,8 +466,8 @@ struct BwdLaunch {
   size_t blocks, groups;
 };
 
-// Teams stay resident: as many blocks as fit the registers (128 a thread).
-// Shifted rows: teams walk rows a multiple of eight apart.
+// Teams stay resident: as many blocks as fit the registers.  Shifted rows:
+// teams walk rows a multiple of eight apart.
 BwdLaunch bwd_launch(size_t rows, size_t cols, int vec, bool shifted) {
   BwdLaunch l;
   if (cols <= static_cast<size_t>(kRowWarpCols)) {
@@ -498,32 +481,35 @@ BwdLaunch bwd_launch(size_t rows, size_t cols, int vec, bool shifted) {
     l.blocks = l.groups = want < fit ? want : fit;
     return l;
   }
+  // Values a thread: 16, or for bf16 32 where one block of 16 a thread would
+  // leave its SM half empty (8192 rows, us for 16 / 32: 5120 columns 58 / 63,
+  // 6144 75 / 68, 7168 80 / 80, 8192 90 / 97) and past 8192 columns (4096
+  // rows: 10240 119 / 62, two blocks of a cluster against one).
   l.lanes = 0;
   l.cluster = 1;
-  if (cols <= kBwdBlockCols) {
-    l.ept = kBwdEpt;
-  } else {
-    l.ept = kStageVecs * vec;
-    while (l.cluster * kBwdThreads * l.ept < static_cast<int>(cols)) l.cluster *= 2;
-  }
+  l.ept = vec == 4 || cols <= 5120 || (cols > 7168 && cols <= 8192) ? 16 : 32;
+  while (static_cast<size_t>(l.cluster) * kBwdThreads * l.ept < cols) l.cluster *= 2;
   const size_t per = static_cast<size_t>(l.ept) * l.cluster;
   l.threads = static_cast<int>(((cols + per - 1) / per + 31) / 32 * 32);
-  const size_t fit = kSmCount / l.cluster * (cols <= kBwdBlockCols ? kBwdThreads / l.threads : 1);
+  // 128 registers a thread leave 512 threads on an SM, the 96 of aligned bf16
+  // at 16 values 640 (1088 columns: 33.6 us against 38.7 with 512)
+  const int resident = vec == 8 && l.ept == 16 && !shifted ? 640 : 512;
+  const size_t fit = kSmCount / l.cluster * (l.cluster == 1 ? resident / l.threads : 1);
   l.groups = rows < fit ? rows : shifted ? fit / 8 * 8 : fit;
   l.blocks = l.groups * l.cluster;
   return l;
 }
 
-template <typename T, int EPT, bool ALIGNED, int LANES, int MAXT>
+template <typename T, int EPT, bool ALIGNED, int LANES>
 cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, LANES, MAXT>, static_cast<unsigned>(l.blocks),
+  return launch_overlapped(rmsnorm_bwd_row_kernel<T, EPT, ALIGNED, LANES>, static_cast<unsigned>(l.blocks),
                            static_cast<unsigned>(l.threads), 0, 1, s, a, partial);
 }
 
-template <typename T, bool ALIGNED, int CL>
+template <typename T, int EPT, bool ALIGNED, int CL>
 cudaError_t launch_staged_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
-  auto kernel = rmsnorm_bwd_staged_kernel<T, ALIGNED, CL>;
-  const size_t smem = size_t{2} * (a.dres ? 3 : 2) * kStageVecs * 16 * l.threads;
+  auto kernel = rmsnorm_bwd_staged_kernel<T, EPT, ALIGNED, CL>;
+  const size_t smem = size_t{2} * (a.dres ? 3 : 2) * EPT * sizeof(T) * l.threads;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -537,16 +523,21 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
   float* partial = a.dgamma ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaErrorInvalidValue;
   if (l.lanes > 0) {
-    if (l.lanes == 8) e = launch_row_kernel<T, 8, ALIGNED, 8, 256>(a, partial, l, s);
-    if (l.lanes == 16) e = launch_row_kernel<T, 8, ALIGNED, 16, 256>(a, partial, l, s);
-    if (l.lanes == 32 && l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 32, 256>(a, partial, l, s);
-    if (l.lanes == 32 && l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 32, 256>(a, partial, l, s);
-    if (l.lanes == 32 && l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 32, 256>(a, partial, l, s);
+    if (l.lanes == 8) e = launch_row_kernel<T, 8, ALIGNED, 8>(a, partial, l, s);
+    if (l.lanes == 16) e = launch_row_kernel<T, 8, ALIGNED, 16>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 8) e = launch_row_kernel<T, 8, ALIGNED, 32>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 16) e = launch_row_kernel<T, 16, ALIGNED, 32>(a, partial, l, s);
+    if (l.lanes == 32 && l.ept == 32) e = launch_row_kernel<T, 32, ALIGNED, 32>(a, partial, l, s);
   } else {
-    if (a.cols <= kBwdBlockCols) e = launch_row_kernel<T, kBwdEpt, ALIGNED, 0, kBwdThreads>(a, partial, l, s);
-    else if (l.cluster == 1) e = launch_staged_kernel<T, ALIGNED, 1>(a, partial, l, s);
-    else if (l.cluster == 2) e = launch_staged_kernel<T, ALIGNED, 2>(a, partial, l, s);
-    else if (l.cluster == 4) e = launch_staged_kernel<T, ALIGNED, 4>(a, partial, l, s);
+    if constexpr (sizeof(T) == 2) {
+      if (l.ept == 32 && l.cluster == 1) e = launch_staged_kernel<T, 32, ALIGNED, 1>(a, partial, l, s);
+      if (l.ept == 32 && l.cluster == 2) e = launch_staged_kernel<T, 32, ALIGNED, 2>(a, partial, l, s);
+      if (l.ept == 16 && l.cluster == 1) e = launch_staged_kernel<T, 16, ALIGNED, 1>(a, partial, l, s);
+    } else {
+      if (l.cluster == 1) e = launch_staged_kernel<T, 16, ALIGNED, 1>(a, partial, l, s);
+      if (l.cluster == 2) e = launch_staged_kernel<T, 16, ALIGNED, 2>(a, partial, l, s);
+      if (l.cluster == 4) e = launch_staged_kernel<T, 16, ALIGNED, 4>(a, partial, l, s);
+    }
   }
   if (e != cudaSuccess || partial == nullptr) return e;
   return launch_join(partial, a.dgamma, a.cols, l.groups, s);
@@ -555,7 +546,7 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
   // rows too long for a cluster's registers, or buffers that lie differently
-  if (a.mode == kRowsAny || a.cols > 4 * kBwdBlockCols)
+  if (a.mode == kRowsAny || a.cols > kRowMaxCols)
     return launch_stream<T>(a, ws, s);
   return a.mode == kRowsAligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
 }
@@ -565,7 +556,7 @@ cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 // Enough for every way the buffers may lie.
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
   const size_t stream = stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
-  if (cols > 4 * kBwdBlockCols || !want_dgamma) return stream;
+  if (cols > kRowMaxCols || !want_dgamma) return stream;
   size_t groups = bwd_launch(rows, cols, vec_elems(dtype), false).groups;
   const size_t shifted = bwd_launch(rows, cols, vec_elems(dtype), true).groups;
   if (shifted > groups) groups = shifted;
