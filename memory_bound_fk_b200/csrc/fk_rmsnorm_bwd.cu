@@ -494,7 +494,9 @@ BwdLaunch bwd_launch(size_t rows, size_t cols, int vec, bool shifted) {
   // 128 registers a thread leave 512 threads on an SM, the 96 of aligned bf16
   // at 16 values 640 (1088 columns: 33.6 us against 38.7 with 512)
   const int resident = vec == 8 && l.ept == 16 && !shifted ? 640 : 512;
-  const size_t fit = kSmCount / l.cluster * (l.cluster == 1 ? resident / l.threads : 1);
+  // (of the clusters of four, 33 run at a time: a second wave took 180 us for
+  // 1024 x 32768 fp32)
+  const size_t fit = l.cluster == 1 ? kSmCount * (resident / l.threads) : l.cluster == 2 ? kSmCount / 2 : 33;
   l.groups = rows < fit ? rows : shifted ? fit / 8 * 8 : fit;
   l.blocks = l.groups * l.cluster;
   return l;
