@@ -591,10 +591,22 @@ def _like(t, name: str, shape, dtype, device: int) -> int:
     shape, type and device index (0 for None)."""
     if t is None:
         return 0
+    if (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     _check_tensor(t, name)
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        raise ValueError(f"{name} must have shape {tuple(shape)} and type {dtype}, on cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {tuple(shape)} and type {dtype}, on cuda:{device}")
+
+
+def _new(lead, n: int | None, dtype, like):
+    """Empty contiguous tensor of the shape [*lead] or [*lead, n] where `like`
+    is.  (One leading dimension is nearly always what there is; empty_strided
+    takes 1.4 us of host time, new_empty 2.0.)"""
+    if len(lead) == 1:
+        m = lead[0]
+        return (_torch.empty_strided((m,), (1,), dtype=dtype, device=like.device) if n is None else
+                _torch.empty_strided((m, n), (n if n > 0 else 1, 1), dtype=dtype, device=like.device))
+    return like.new_empty(lead if n is None else (*lead, n), dtype=dtype)
 
 
 def _rows_input(x, name: str):
@@ -641,7 +653,7 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out_dtype=None, ou
     elif cols == 0:
         raise ValueError("rows without columns have no scale")
     elif scales is None:
-        scales = x.new_empty(shape[:-1], dtype=torch.float32)
+        scales = _new(shape[:-1], None, torch.float32, x)
         p_scales = scales.data_ptr()
     else:
         p_scales = _like(scales, "scales", shape[:-1], torch.float32, dev)
@@ -681,7 +693,7 @@ def rmsnorm_backward(dy, h, weight=None, eps: float = 1e-6, dresidual=None, out=
         if dweight is not None:
             raise ValueError("dweight given, but need_dweight is false")
     elif dweight is None:
-        dweight = h.new_empty((cols,), dtype=torch.float32)
+        dweight = _new((cols,), None, torch.float32, h)
         p_dw = dweight.data_ptr()
     else:
         p_dw = _like(dweight, "dweight", (cols,), torch.float32, dev)
@@ -729,7 +741,7 @@ def quantize_rows(x, dtype=None, gelu: str | None = None, out=None, scales=None)
     else:
         p_out = _like(out, "out", shape, dtype, x.get_device())
     if scales is None:
-        scales = x.new_empty(shape[:-1], dtype=torch.float32)
+        scales = _new(shape[:-1], None, torch.float32, x)
         p_scales = scales.data_ptr()
     else:
         p_scales = _like(scales, "scales", shape[:-1], torch.float32, x.get_device())
@@ -770,7 +782,7 @@ def matmul_q8(a, a_scales, b, b_scales, bias=None, gelu: str | None = None, out_
     if out_code is None:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     if out is None:
-        out = a.new_empty((*lead, n), dtype=out_dtype)
+        out = _new(lead, n, out_dtype, a)
         p_out = out.data_ptr()
     else:
         p_out = _like(out, "out", (*lead, n), out_dtype, dev)
