@@ -16,6 +16,9 @@
 //
 // The product is bound by reading B once while m is below about 250 (B at
 // 6.5 TB/s against 2 m ops a byte at 3.4 POP/s), by the tensor cores above.
+// Measured on B200 in a captured chain (int8 to bf16): 1 x 16384 x 4096 13.3
+// us (5.0 TB/s of B; alone 10.3 at the copy's rate, the rest is the start and
+// the last blocks), 48 x 32001 x 4096 to fp32 24 us (5.7 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -199,7 +202,9 @@ __global__ void __launch_bounds__(kMmThreads)
 
 // ---------------------------------------------------------------- rows padded to 16 bytes
 
-// dst [rows, kp] <- src [rows, k] (any alignment), zeros past k; kp is k
+// For operands TMA cannot read (a pitch that is no multiple of 16 bytes): one
+// more write and read of them, which a caller avoids by keeping k a multiple
+// of 16.  dst [rows, kp] <- src [rows, k] (any alignment), zeros past k; kp is k
 // rounded up to 16.  One thread per 16 bytes of dst: five aligned words and a
 // funnel shift, or single bytes next to the ends of src.
 __global__ void __launch_bounds__(256)

@@ -20,6 +20,12 @@ constexpr size_t kMaxGrid = 0x7fffffffu;
 
 // ---------------------------------------------------------------- rows held in registers
 
+// One team per row: it is read, kept, reduced and written (fk_q8_rows.cuh).
+// Bound by HBM; measured on B200, event overhead taken off: 16384 x 4096
+// bf16 + residual to e4m3 and h 77 us (6.1 TB/s), to bf16 81 (6.6 TB/s), the
+// same in fp32 158 (6.8 TB/s); 4096 x 16384 bf16 to e4m3 85; one row of 4096
+// 2.2 us.  Clusters that share a row, and 16 values a thread in place of 32,
+// were slower.
 // MAXT, MINB: threads and blocks per SM the registers are sized for (64 a
 // thread for 1024 threads on an SM).
 template <typename T, int OUT, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB>
@@ -110,6 +116,8 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
 // One 512-thread block per row, which reads the row twice: statistics (and
 // h stored), then the outputs.  Any length and alignment.  Plain loads: the
 // second pass re-reads h where it was stored, which may be x or residual.
+// Value by value, for rows past 32768 columns and buffers that lie
+// differently to 16 bytes: 1024 x 49152 bf16 + residual to bf16 220 us.
 template <typename T, int OUT>
 __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormArgs a) {
   constexpr bool Q8 = OUT == FK_I8 || OUT == FK_E4M3;

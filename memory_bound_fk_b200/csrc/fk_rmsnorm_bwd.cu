@@ -37,7 +37,9 @@ constexpr size_t kStreamGroups = 64;  // groups of rows on the streaming path
 // gamma and the running dgamma sums live in its registers.  The next row's h
 // and dy are loaded before the current one is reduced, which keeps HBM busy
 // through the reduction.  At the end each block adds its warps' sums in order
-// and writes them, one row of workspace per block.
+// and writes them, one row of workspace per block.  Bound by HBM; measured
+// on B200: 200000 x 64 fp32 with dres 37 us (5.6 TB/s), 20000 x 1024 fp32 55
+// (5.9), 20000 x 1024 bf16 32 (5.2).
 template <typename T, int EPT, bool ALIGNED, int LANES>
 __global__ void __launch_bounds__(32 * kRowWarps, EPT == 32 ? 1 : EPT == 16 ? 2 : small_blocks(Elem<T>::VEC))
     rmsnorm_bwd_row_kernel(const __grid_constant__ RmsnormBwdArgs a, float* partial) {
@@ -338,6 +340,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 // ---------------------------------------------------------------- streaming path
 
+// Value by value, for rows past 32768 columns and buffers that lie
+// differently to 16 bytes, in four kernels: dy and h are read three times
+// (1024 x 49152 bf16 with dres: 315 us).
 // Row statistics: (r, r^2 s) of every row, one block per row.
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads) rmsnorm_bwd_stats_kernel(RmsnormBwdArgs a, float2* stats) {
@@ -387,7 +392,8 @@ __global__ void __launch_bounds__(kColThreads)
 }
 
 // dgamma_j = sum of the groups' partial sums: 32 columns per block, every
-// 32nd group to each of its 32 warps, the warps' sums added in order.
+// 32nd group to each of its 32 warps, the warps' sums added in order.  About
+// 3 us behind the first step (4.8 MB of partial sums from L2 for 4096 columns).
 __global__ void __launch_bounds__(kJoinCols* kJoinWays)
     rmsnorm_bwd_join_kernel(const float* partial, float* dgamma, size_t cols, size_t groups) {
   __shared__ float part[kJoinWays][kJoinCols];
@@ -459,7 +465,7 @@ cudaError_t launch_stream(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// How the registers-resident kernel is launched for a shape: blocks, threads,
+// How the kernel of resident teams is launched for a shape: blocks, threads,
 // blocks per team, rows of partial sums.
 struct BwdLaunch {
   int lanes, ept, cluster, threads;  // cluster: 0 for warp teams
@@ -547,7 +553,7 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
-  // rows too long for a cluster's registers, or buffers that lie differently
+  // rows too long for a cluster's shared memory, or buffers that lie differently
   if (a.mode == kRowsAny || a.cols > kRowMaxCols)
     return launch_stream<T>(a, ws, s);
   return a.mode == kRowsAligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
