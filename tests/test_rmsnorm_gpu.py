@@ -374,3 +374,18 @@ def test_backward_of_tiny_rows(fk, torch_mod, cols):
     got = backward(fk, torch_mod, dy, h, g, None, True, 0.0)
     assert np.isfinite(got[0]).all() and np.abs(got[0]).max() > 1e13
     check_backward(dy, h, g, None, got, 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1500, 1056), (700, 5120), (330, 6144), (500, 16384), (333, 16383), (401, 12288), (250, 32768),
+                                       (161, 32767)])
+def test_backward_many_rows_a_team(fk, torch_mod, rows, cols, dtype):
+    """Long rows, several to each resident team: every place of the two that are staged is used again, in place too."""
+    dy, h, dr = (make_rows(rows, cols, dtype, cols + i, 0.3) for i in range(3))
+    g = gamma_of(cols, cols)
+    want = backward(fk, torch_mod, dy, h, g, dr)
+    check_backward(dy, h, g, dr, want)
+    for alias in ("dy", "h", "dres"):
+        got = backward(fk, torch_mod, dy, h, g, dr, alias=alias)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    check_backward(dy, h, g, None, backward(fk, torch_mod, dy, h, g, None))
