@@ -66,10 +66,12 @@ typedef enum fk_q8type {
  * stands), and y == x or y == residual when out_dtype == dtype and h is
  * elsewhere.  Every other overlap of an output with an input or another
  * output is rejected.
- * Arithmetic in fp32.  The row is read once up to 32768 columns; longer rows
+ * Arithmetic in fp32.  The row is read once up to 131072 columns; longer rows
  * are read twice.  A row whose h holds a NaN or an infinity, or whose sum of
  * squares overflows fp32 (|h| past about 1e19), is NaN throughout (8-bit:
- * scale NaN, codes 0).  eps == 0 makes a row of zeros NaN.
+ * scale NaN, codes 0).  eps == 0 makes a row of zeros NaN, and a row of
+ * values whose squares underflow (below about 1e-22) counts as one.  The
+ * products h_j gamma_j have to lie within fp32's range.
  * Errors: FK_ERR_INVALID_ARG for bad pointers, overlap, eps, scales present
  * or absent against out_dtype, or h without residual;
  * FK_ERR_UNSUPPORTED_DTYPE for another dtype or out_dtype.
@@ -95,7 +97,7 @@ FK_API fk_status fk_rmsnorm_rows(const void *x, const void *residual, const floa
  *   dgamma [out] cols fp32 values, or NULL (not computed).  rows == 0 gives 0.
  *   eps    as in the forward call.
  * Arithmetic in fp32; dgamma is summed in fp32 in an order fixed by the
- * shape (two equal calls give equal bits).  Rows up to 32768 columns are
+ * shape (two equal calls give equal bits).  Rows up to 65536 columns are
  * read once.
  * Errors as fk_rmsnorm_rows; dgamma must overlap nothing.
  */
@@ -124,7 +126,7 @@ FK_API fk_status fk_rmsnorm_rows_bwd_ws(const void *dy, const void *h, const flo
  *   epilogue  an fk_epilogue: the values are quantised as they are, or
  *             through GELU in either form (computed in fp32, with the
  *             accuracy of fk_gelu on FK_F32).
- * The row is read once up to 32768 columns, twice beyond.
+ * The row is read once up to 131072 columns, twice beyond.
  * Weights [n, k] become per-channel scales by the same call.
  */
 FK_API fk_status fk_quantize_rows(const void *x, void *q, float *scales, size_t rows, size_t cols, int dtype,

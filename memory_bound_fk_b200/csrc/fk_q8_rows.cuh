@@ -32,7 +32,8 @@ constexpr int kRowLaneEpt = 8;         // values a thread where a row takes 8 or
 constexpr int kRowWarpCols = 1024;     // rows up to here take one warp
 constexpr int kRowBlockCols = 8192;    // RMSNorm: up to here four vectors a thread (fp32: 512 threads)
 constexpr int kRowLargeCols = 16384;   // up to here 32 values a thread, at most 512 threads
-constexpr int kRowMaxCols = 32768;     // the same, at most 1024 threads; longer rows are streamed
+constexpr int kRowMaxCols = 32768;     // the same, at most 1024 threads
+constexpr int kRowClusterCols = 131072;  // clusters of 4 or 8 such blocks of 512 threads; longer rows are streamed
 constexpr size_t kRowMaxGrid = 0x7fffffffu;
 
 // A thread's place in its team; the row's columns, how many of them come
@@ -217,6 +218,24 @@ __device__ __forceinline__ void team_sum_max(float& s, float& m, float2* red) {
   }
 }
 
+// The same over the CL blocks of a cluster (`red`: one pair per warp of the
+// cluster).  Every block has started (cluster_wait()); used once.
+template <int CL>
+__device__ __forceinline__ void cluster_sum_max(float& s, float& m, float2* red) {
+  warp_sum_max(s, m);
+  const int warps = static_cast<int>(blockDim.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  if (lane < CL)
+    st_cluster_f2(cluster_addr(&red[static_cast<int>(cluster_ctarank()) * warps + static_cast<int>(threadIdx.x >> 5)], lane),
+                  s, m);
+  cluster_barrier();
+  s = red[0].x;
+  m = red[0].y;
+  for (int w = 1; w < CL * warps; ++w) {
+    s += red[w].x;
+    m = absmax_nan(m, red[w].y);
+  }
+}
+
 // The maximum alone (of values: NaN if one is; at least 0 over a block).
 // `red`: 16-byte aligned, one word per warp, their number rounded up to four.
 template <int LANES>
@@ -243,10 +262,16 @@ __device__ __forceinline__ void team_max(float& m, float* red) {
 
 // Calls fn(row, t, team, cols) for the rows of this block: 32 / LANES rows per
 // warp, or (LANES = 0) one per block at a time.  Lanes of a warp that have no
-// row left take part with no columns.
-template <int LANES, typename F>
+// row left take part with no columns.  CL > 1: one row per cluster of CL
+// blocks (their number is that of the rows times CL).
+template <int LANES, int CL, typename F>
 __device__ __forceinline__ void for_rows(size_t rows, int cols, F fn) {
-  if constexpr (LANES > 0) {
+  if constexpr (CL > 1) {
+    cluster_arrive_relaxed();
+    cluster_wait();  // every block has started
+    fn(blockIdx.x / CL, static_cast<int>(cluster_ctarank() * blockDim.x + threadIdx.x),
+       static_cast<int>(CL * blockDim.x), cols);
+  } else if constexpr (LANES > 0) {
     constexpr int PER = 32 / LANES;
     const size_t per = (blockDim.x >> 5) * PER, stride = gridDim.x * per;
     const int lane = threadIdx.x & 31;
@@ -289,6 +314,13 @@ inline RowLaunch warp_launch(size_t rows, int lanes) {
 inline RowLaunch block_launch(size_t rows, size_t cols, int ept) {
   const size_t threads = ((cols + ept - 1) / ept + 31) / 32 * 32;
   return {static_cast<unsigned>(rows < kRowMaxGrid ? rows : kRowMaxGrid), static_cast<unsigned>(threads)};
+}
+
+// One cluster of `cl` blocks per row at 32 values a thread (no blocks, which
+// the launch refuses, past the largest grid).
+inline RowLaunch cluster_launch(size_t rows, size_t cols, int cl) {
+  const size_t per = size_t{32} * cl, threads = ((cols + per - 1) / per + 31) / 32 * 32;
+  return {static_cast<unsigned>(rows <= kRowMaxGrid / cl ? rows * cl : 0), static_cast<unsigned>(threads)};
 }
 
 }  // namespace

@@ -118,13 +118,14 @@ __device__ __forceinline__ float max_words(float m, const uint4& w) {
 // e4m3 31.6 us (6.4 TB/s), through the tanh form 37.5 (two MUFU operations a
 // value take 30), through the erf form 62; 8192 x 8192 fp32 50 / 53 / 64.
 // MAXT, MINB as in fk_rmsnorm.cu.
-template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB>
+template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB, int CL = 1>
 __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_constant__ QuantizeArgs a) {
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
   __shared__ __align__(16) float red[LANES ? 1 : MAXT / 32];
+  __shared__ float2 pairs[CL > 1 ? CL * (MAXT / 32) : 1];
   let_next_start();
   after_previous();
-  for_rows<LANES>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
+  for_rows<LANES, CL>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
     const size_t base = row * a.cols;
     const T* const x = static_cast<const T*>(a.x) + base;
     uint8_t* const o = static_cast<uint8_t*>(a.q) + base;
@@ -151,7 +152,12 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_c
       ev = act<EPI>(ev);
       m = absmax_nan(m, ev);
     }
-    team_max<LANES>(m, red);
+    if constexpr (CL > 1) {
+      float none = 0.0f;
+      cluster_sum_max<CL>(none, m, pairs);
+    } else {
+      team_max<LANES>(m, red);
+    }
     const RowScale q = row_scale<OUT>(m);
     if (t == 0 && cols > 0) a.scales[row] = q.scale;
 #pragma unroll
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_
 
 // One 512-thread block per row, which reads the row twice: the largest
 // magnitude, then the codes.  Any length and alignment; value by value, for
-// rows past 32768 columns (2048 x 49152 bf16 to e4m3: 128 us).
+// rows past 131072 columns (2048 x 49152 bf16 to e4m3: 128 us).
 template <typename T, int OUT, int EPI>
 __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(QuantizeArgs a) {
   __shared__ float2 red[kStreamThreads / 32];
@@ -301,12 +307,17 @@ cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
   }
   if (a.cols <= kRowLargeCols)
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  if (a.cols <= kRowMaxCols)
+    return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  const int cl = a.cols <= kRowClusterCols / 2 ? 4 : 8;
+  const RowLaunch c = cluster_launch(a.rows, a.cols, cl);
+  return cl == 4 ? launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2, 4>, c.grid, c.threads, 0, 4, s, a)
+                 : launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2, 8>, c.grid, c.threads, 0, 8, s, a);
 }
 
 template <typename T, int OUT, int EPI>
 cudaError_t launch_epi(const QuantizeArgs& a, cudaStream_t s) {
-  if (a.cols > kRowMaxCols) {
+  if (a.cols > kRowClusterCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     return launch_overlapped(quantize_stream_kernel<T, OUT, EPI>, g, kStreamThreads, 0, 1, s, a);
   }

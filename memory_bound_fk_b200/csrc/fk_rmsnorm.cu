@@ -28,15 +28,15 @@ constexpr size_t kMaxGrid = 0x7fffffffu;
 // were slower.
 // MAXT, MINB: threads and blocks per SM the registers are sized for (64 a
 // thread for 1024 threads on an SM).
-template <typename T, int OUT, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB>
+template <typename T, int OUT, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB, int CL = 1>
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_constant__ RmsnormArgs a) {
   constexpr bool Q8 = OUT == FK_I8 || OUT == FK_E4M3;
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
-  __shared__ float2 red[LANES ? 1 : MAXT / 32];
+  __shared__ float2 red[LANES ? 1 : CL * (MAXT / 32)];
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   let_next_start();
   after_previous();
-  for_rows<LANES>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
+  for_rows<LANES, CL>(a.rows, static_cast<int>(a.cols), [&](size_t row, int t, int team, int cols) {
     const size_t base = row * a.cols;
     const T* const x = static_cast<const T*>(a.x) + base;
     const T* const res = static_cast<const T*>(a.residual) + base;
@@ -85,7 +85,10 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
       if (a.gamma) ev *= __ldg(a.gamma + edge);
       if (Q8) m = absmax_nan(m, ev);
     }
-    team_sum_max<LANES>(s, m, red);
+    if constexpr (CL > 1)
+      cluster_sum_max<CL>(s, m, red);
+    else
+      team_sum_max<LANES>(s, m, red);
     const float rstd = rms_rstd(s, inv_n, a.eps);
     RowScale q;
     if constexpr (Q8) {
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
 // One 512-thread block per row, which reads the row twice: statistics (and
 // h stored), then the outputs.  Any length and alignment.  Plain loads: the
 // second pass re-reads h where it was stored, which may be x or residual.
-// Value by value, for rows past 32768 columns and buffers that lie
+// Value by value, for rows past 131072 columns and buffers that lie
 // differently to 16 bytes: 1024 x 49152 bf16 + residual to bf16 220 us.
 template <typename T, int OUT>
 __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormArgs a) {
@@ -188,12 +191,17 @@ cudaError_t launch_rows(const RmsnormArgs& a, cudaStream_t s) {
   const RowLaunch l = block_launch(a.rows, a.cols, 32);
   if (a.cols <= kRowLargeCols)
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  if (a.cols <= kRowMaxCols)
+    return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  const int cl = a.cols <= kRowClusterCols / 2 ? 4 : 8;
+  const RowLaunch c = cluster_launch(a.rows, a.cols, cl);
+  return cl == 4 ? launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 512, 2, 4>, c.grid, c.threads, 0, 4, s, a)
+                 : launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 512, 2, 8>, c.grid, c.threads, 0, 8, s, a);
 }
 
 template <typename T, int OUT>
 cudaError_t launch_out(const RmsnormArgs& a, cudaStream_t s) {
-  if (a.mode == kRowsAny || a.cols > kRowMaxCols) {
+  if (a.mode == kRowsAny || a.cols > kRowClusterCols) {
     const unsigned g = static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     return launch_overlapped(rmsnorm_stream_kernel<T, OUT>, g, kStreamThreads, 0, 1, s, a);
   }

@@ -24,6 +24,7 @@ constexpr size_t kMaxGrid = 0x7fffffffu;
 constexpr int kColThreads = 128;      // columns per block of the column sums
 constexpr int kJoinCols = 32, kJoinWays = 32;
 constexpr int kBwdThreads = 512;      // of a block whose rows are staged, at most
+constexpr int kBwdMaxCols = 65536;    // longer rows are streamed
 // Blocks per SM of warp teams with 8 values a lane (registers follow): 200000 x
 // 64 fp32 29 us at three and 35 at four, 100000 x 128 bf16 27 and 25.
 constexpr int small_blocks(int vec) { return vec == 8 ? 4 : 3; }
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 // ---------------------------------------------------------------- streaming path
 
-// Value by value, for rows past 32768 columns and buffers that lie
+// Value by value, for rows past 65536 columns and buffers that lie
 // differently to 16 bytes, in four kernels: dy and h are read three times
 // (1024 x 49152 bf16 with dres: 315 us).
 // Row statistics: (r, r^2 s) of every row, one block per row.
@@ -500,9 +501,12 @@ BwdLaunch bwd_launch(size_t rows, size_t cols, int vec, bool shifted) {
   // 128 registers a thread leave 512 threads on an SM, the 96 of aligned bf16
   // at 16 values 640 (1088 columns: 33.6 us against 38.7 with 512)
   const int resident = vec == 8 && l.ept == 16 && !shifted ? 640 : 512;
-  // (of the clusters of four, 33 run at a time: a second wave took 180 us for
+  // (of the clusters of four 33 run at a time, of those of eight 15: a second wave took 180 us for
   // 1024 x 32768 fp32)
-  const size_t fit = l.cluster == 1 ? kSmCount * (resident / l.threads) : l.cluster == 2 ? kSmCount / 2 : 33;
+  const size_t fit = l.cluster == 1   ? kSmCount * (resident / l.threads)
+                     : l.cluster == 2 ? kSmCount / 2
+                     : l.cluster == 4 ? 33
+                                      : 15;
   l.groups = rows < fit ? rows : shifted ? fit / 8 * 8 : fit;
   l.blocks = l.groups * l.cluster;
   return l;
@@ -540,11 +544,13 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
       if (l.ept == 32 && l.cluster == 1) e = launch_staged_kernel<T, 32, ALIGNED, 1>(a, partial, l, s);
       if (l.ept == 32 && l.cluster == 2) e = launch_staged_kernel<T, 32, ALIGNED, 2>(a, partial, l, s);
+      if (l.ept == 32 && l.cluster == 4) e = launch_staged_kernel<T, 32, ALIGNED, 4>(a, partial, l, s);
       if (l.ept == 16 && l.cluster == 1) e = launch_staged_kernel<T, 16, ALIGNED, 1>(a, partial, l, s);
     } else {
       if (l.cluster == 1) e = launch_staged_kernel<T, 16, ALIGNED, 1>(a, partial, l, s);
       if (l.cluster == 2) e = launch_staged_kernel<T, 16, ALIGNED, 2>(a, partial, l, s);
       if (l.cluster == 4) e = launch_staged_kernel<T, 16, ALIGNED, 4>(a, partial, l, s);
+      if (l.cluster == 8) e = launch_staged_kernel<T, 16, ALIGNED, 8>(a, partial, l, s);
     }
   }
   if (e != cudaSuccess || partial == nullptr) return e;
@@ -554,7 +560,7 @@ cudaError_t launch_rows(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
   // rows too long for a cluster's shared memory, or buffers that lie differently
-  if (a.mode == kRowsAny || a.cols > kRowMaxCols)
+  if (a.mode == kRowsAny || a.cols > kBwdMaxCols)
     return launch_stream<T>(a, ws, s);
   return a.mode == kRowsAligned ? launch_rows<T, true>(a, ws, s) : launch_rows<T, false>(a, ws, s);
 }
@@ -564,7 +570,7 @@ cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 // Enough for every way the buffers may lie.
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
   const size_t stream = stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
-  if (cols > kRowMaxCols || !want_dgamma) return stream;
+  if (cols > kBwdMaxCols || !want_dgamma) return stream;
   size_t groups = bwd_launch(rows, cols, vec_elems(dtype), false).groups;
   const size_t shifted = bwd_launch(rows, cols, vec_elems(dtype), true).groups;
   if (shifted > groups) groups = shifted;
