@@ -307,8 +307,19 @@ cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
   }
   if (a.cols <= kRowLargeCols)
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
-  if (a.cols <= kRowMaxCols)
+  if constexpr (sizeof(T) == 2 && EPI != FK_EPILOGUE_NONE) {
+    // two blocks of 512 threads to a row compute one row while another loads
+    // (4096 rows, tanh form, us against one block of 1024: 20000 columns 67
+    // and 92, 24576 95 and 103, 32768 113 and 130; without GELU, 32768: 89
+    // and 87)
+    if (a.cols <= kRowMaxCols) {
+      const RowLaunch c = cluster_launch(a.rows, a.cols, 2);
+      return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2, 2>, c.grid, c.threads, 0, 2, s, a);
+    }
+  } else if (a.cols <= kRowMaxCols) {
     return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
+  }
+  // 4 or 8 blocks of 512 threads (1024 x 65536 bf16 54 us; 2 or 4 of 1024: 60)
   const int cl = a.cols <= kRowClusterCols / 2 ? 4 : 8;
   const RowLaunch c = cluster_launch(a.rows, a.cols, cl);
   return cl == 4 ? launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2, 4>, c.grid, c.threads, 0, 4, s, a)
