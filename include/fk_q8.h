@@ -153,7 +153,8 @@ FK_API fk_status fk_quantize_rows(const void *x, void *q, float *scales, size_t 
  * bias added, act applied, and rounded once to `out_dtype`.  Two equal calls
  * give equal bits.  k a multiple of 16 with a and b 16-byte aligned runs
  * without workspace; otherwise a and b are first copied to workspace rows
- * padded with zeros to a multiple of 16.
+ * padded with zeros to a multiple of 16, whole 128-byte lines apart.  (k a
+ * multiple of 128 is best: other pitches make TMA read across lines.)
  * Errors: FK_ERR_INVALID_ARG for a shape outside the above, bad pointers or
  * overlap; FK_ERR_UNSUPPORTED_DTYPE for another dtype or out_dtype.
  * A wait that gives up inside the kernel (see fk_wait_timeouts) leaves that

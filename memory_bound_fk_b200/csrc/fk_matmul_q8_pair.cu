@@ -389,7 +389,7 @@ cudaError_t launch_shape(const Call& c) {
   const size_t tiles_n = (c.p.n + 2 * kChan - 1) / (2 * kChan), tiles_m = (c.p.m + TOK - 1) / TOK;
   if (tiles_m > 0x7fffffffu / kGroup / 2 / tiles_n) return cudaErrorInvalidConfiguration;
   CUtensorMap ma, mb;
-  if (!make_map(&ma, c.a, c.p.m, c.k, c.pitch, TOK / 2) || !make_map(&mb, c.b, c.p.n, c.k, c.pitch, kChan))
+  if (!make_map(&ma, c.a, c.p.m, c.k, c.pitch_a, TOK / 2) || !make_map(&mb, c.b, c.p.n, c.k, c.pitch_b, kChan))
     return cudaErrorInvalidValue;
   void (*kernel)(CUtensorMap, CUtensorMap, Params);
   if constexpr (SPLIT == 0)

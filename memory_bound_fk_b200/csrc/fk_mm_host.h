@@ -22,11 +22,11 @@ struct Params {
   int tiles_n, tiles_m;
 };
 
-// A product whose operands TMA can read: [m, k] and [n, k] with a row pitch
-// that is a multiple of 16 bytes.
+// A product whose operands TMA can read: [m, k] and [n, k] with row pitches
+// that are multiples of 16 bytes.
 struct Call {
   const void *a, *b;
-  size_t k, pitch;
+  size_t k, pitch_a, pitch_b;
   MatmulQ8Args p;
   int sm_count;
   cudaStream_t stream;

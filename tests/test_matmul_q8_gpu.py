@@ -113,6 +113,16 @@ def test_any_k_and_misaligned(fk, torch_mod, m, n, k, kind):
     check(*ops, "bf16", None, run(fk, torch_mod, *ops, "bf16", off=(0, 0, 1)))
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 17, 2049), (3, 50, 4097), (90, 9, 6145), (2, 700, 2031), (1, 1, 1), (2, 3, 16385)])
+def test_rows_copied_in_several_strips(fk, torch_mod, m, n, k):
+    """The copies of operands off 16 bytes, around the 2048 codes that a warp takes of a row, at every lead."""
+    ops = operands(torch_mod, m, n, k, "i8", bias=False, seed=k)
+    want = run(fk, torch_mod, *ops, "f32")
+    check(*ops, "f32", None, want)
+    for off in range(1, 16, 2):
+        assert np.array_equal(want, run(fk, torch_mod, *ops, "f32", off=(off, 16 - off, 0)))
+
+
 @pytest.mark.parametrize("m,n", [(1, 64), (40, 200), (300, 260)])
 def test_int8_sums_are_exact_at_the_largest_k(fk, torch_mod, m, n):
     """All codes -128 at k = 131071: the sum 2147467264 is below 2^31."""
