@@ -521,9 +521,12 @@ cudaError_t launch_row_kernel(const RmsnormBwdArgs& a, float* partial, const Bwd
 template <typename T, int EPT, bool ALIGNED, int CL>
 cudaError_t launch_staged_kernel(const RmsnormBwdArgs& a, float* partial, const BwdLaunch& l, cudaStream_t s) {
   auto kernel = rmsnorm_bwd_staged_kernel<T, EPT, ALIGNED, CL>;
-  const size_t smem = size_t{2} * (a.dres ? 3 : 2) * EPT * sizeof(T) * l.threads;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the limit is the kernel's, not the call's: it may not fall under another
+  // thread's launch
+  constexpr size_t per_thread = 2 * EPT * sizeof(T);
+  const size_t smem = per_thread * (a.dres ? 3 : 2) * l.threads;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(per_thread * 3 * kBwdThreads));
   if (e != cudaSuccess) return e;
   return launch_overlapped(kernel, static_cast<unsigned>(l.blocks), static_cast<unsigned>(l.threads), smem, CL, s, a,
                            partial);

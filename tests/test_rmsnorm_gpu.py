@@ -389,3 +389,36 @@ def test_backward_many_rows_a_team(fk, torch_mod, rows, cols, dtype):
         got = backward(fk, torch_mod, dy, h, g, dr, alias=alias)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
     check_backward(dy, h, g, None, backward(fk, torch_mod, dy, h, g, None))
+
+
+def test_calls_from_two_threads(fk, torch_mod):
+    """Two host threads, each on its stream, with shapes that share a kernel and differ in its shared memory."""
+    import threading
+
+    torch = torch_mod
+    cases = [(300, 1100, False), (300, 8192, True), (40, 16384, True), (64, 1056, False)]
+    data, want, got, errors = [], [], [None] * len(cases), []
+    for i, (rows, cols, res) in enumerate(cases):
+        t = [make_rows(rows, cols, "f32", 10 * i + j).cuda() for j in range(3)]
+        data.append((t[0], t[1], t[2] if res else None))
+        want.append(fk.rmsnorm_backward(t[0], t[1], dresidual=data[i][2]))
+    torch.cuda.synchronize()
+
+    def work(mine):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    for i in mine:
+                        got[i] = fk.rmsnorm_backward(data[i][0], data[i][1], dresidual=data[i][2])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(m,)) for m in ((0, 2), (1, 3))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
