@@ -1,7 +1,8 @@
 // fk_q8_rows.cuh -- the register-resident row pass shared by RMSNorm and the
-// row quantiser (sm_100a): a team of threads (a warp, or a block of as many
-// warps as the row needs) reads a row once, keeps its values in registers as
-// fp32, reduces them once, and writes the outputs.
+// row quantiser (sm_100a): a team of threads (part of a warp, a warp, a block
+// of as many warps as the row needs, or a cluster of them) reads a row once,
+// keeps its values in registers as fp32, reduces them once, and writes the
+// outputs.
 //
 // Placement: 16-byte vectors of VEC values; thread t of the team holds vectors
 // t, team + t, 2 team + t, ..., so a warp's accesses are contiguous.  Rows

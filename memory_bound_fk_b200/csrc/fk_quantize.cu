@@ -50,7 +50,7 @@ __device__ __forceinline__ float2 act2_joint(float2 x) {
   if constexpr (EPI == FK_EPILOGUE_GELU_TANH) {
     const float2 a = mul2(x, fma2(splat2(kB), mul2(x, x), splat2(kA)));
     const float2 s = add2(make_float2(ex2_ftz(a.y), ex2_ftz(a.x)), splat2(1.0f));  // the other's
-    return mul2(mul2(x, s), splat2(rcp_approx(s.x * s.y)));
+    return mul2(x, mul2(s, splat2(rcp_approx(s.x * s.y))));  // (x s could overflow)
   }
   if constexpr (EPI == FK_EPILOGUE_GELU_ERF) {
     const float2 w = mul2(make_float2(fabsf(x.x), fabsf(x.y)), splat2(kRsqrt2));

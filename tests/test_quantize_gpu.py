@@ -126,6 +126,25 @@ def test_gelu_of_special_rows(fk, torch_mod, cols, dtype, gelu):
         assert np.isnan(s[[5, 6, 8]]).all() and np.isfinite(s[[0, 1, 2, 3, 4, 7, 9, 10]]).all()
 
 
+@pytest.mark.parametrize("gelu", ["tanh", "erf"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [64, 4096, 16384, 20000])
+def test_gelu_of_far_values_next_to_each_other(fk, torch_mod, cols, dtype, gelu):
+    """Large and far negative values side by side, in either order: what one
+    of them exponentiates must not reach the other."""
+    x = make_rows(4, cols, dtype, cols + 6)
+    x[0, 0] = 1.0e30
+    x[0, 2::4], x[0, 3::4] = 1.0e27, -9.0
+    x[1, 1] = 3.0e38
+    x[1, 2::4], x[1, 3::4] = -40.0, 2.0e37
+    x[2] = -7.4
+    x[2, 1::2] = 0.4
+    x[3] = -7.6
+    x[3, ::2] = 60.0
+    for kind in ("i8", "e4m3"):
+        check(x, kind, gelu, run(fk, torch_mod, x, kind, gelu))
+
+
 @pytest.mark.parametrize("kind", ["i8", "e4m3"])
 def test_every_code_and_ties(fk, torch_mod, kind):
     """Rows built to hit every code exactly, and every border between two:
