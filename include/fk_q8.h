@@ -27,9 +27,11 @@
  * Q = 127 (FK_I8, symmetric: -128 never appears) or 448 (FK_E4M3), rounding
  * to nearest even; the value a code stands for is code * scale.  A row of
  * zeros has codes 0.  A row holding a NaN or an infinity has the scale NaN
- * and codes 0, so everything computed from it is NaN.  v_j / scale is
- * evaluated as v_j * (Q / max) in fp32: a value within about 3 * 2^-24
- * (relative) of a border between two codes may take either.
+ * and codes 0, so everything computed from it is NaN.  In fp32: the scale is
+ * the product of the maximum and 1 / Q rounded, v_j / scale the quotient
+ * rounded, and that is rounded to the code: scales and codes of given values
+ * are those of torch's v.abs().amax(-1) / Q and v / scale on the GPU.  (Rows whose largest magnitude is past
+ * 2^110 aside, where the quotient's last bit may differ.)
  */
 #ifndef FK_Q8_H
 #define FK_Q8_H

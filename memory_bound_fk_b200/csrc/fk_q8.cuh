@@ -1,10 +1,21 @@
 // fk_q8.cuh -- 8-bit codes and per-row scales: the conversions and the row
 // reductions shared by RMSNorm and the row quantiser (sm_100a).
 //
-// A row v becomes scale = max(max |v_j|, 2^-100) / Q and code_j =
-// round(v_j * (Q / max)), nearest even (Q = 127 or 448).  The lower limit on
-// the maximum keeps Q / max finite, so a row of zeros needs no special case.
-// v_j * (Q / max) exceeds Q by at most a rounding, which rounds back to Q.
+// A row v becomes scale = max(max |v_j|, 2^-100) * (1 / Q) and code_j =
+// round(v_j / scale), nearest even (Q = 127 or 448; 1 / Q rounded to fp32, as
+// torch divides a tensor by a number on the GPU).  The lower limit on the
+// maximum keeps 1 / scale finite, so a row of zeros needs no special case.
+// v_j / scale exceeds Q by at most a rounding, which rounds back to Q.
+//
+// The quotient is that of the stored fp32 scale, rounded once: values of bf16
+// rows stand often exactly on a border between two codes of max / Q, and go
+// the way that v / scale takes them in any fp32 arithmetic.  With 1 / scale in
+// two fp32 terms, hi = rounded and lo = hi (1 - scale hi) (the remainder comes
+// out of one fused multiply-add without error), v hi + v lo in one FMA is
+// within 2^-47 of v / scale before its rounding.  One packed instruction a
+// pair more than v hi alone; correcting v hi by its own remainder takes two
+// (8192 x 16384 bf16 through GELU to e4m3, against v hi alone: 3.9% and 7.5%
+// more time; without GELU, and in the norm, under 2%).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,26 +45,39 @@ __device__ __forceinline__ float absmax_nan(float a, float b) {
   return r;
 }
 
+// What a row's codes are made with: the stored scale, and its reciprocal in two
+// terms; a row that is not finite gets the scale NaN and codes 0 (`ok`).
+struct RowScale {
+  float scale, hi, lo;
+  bool ok;
+};
+
+// v / scale, rounded once.
+__device__ __forceinline__ float over_scale(float v, const RowScale& q) { return fmaf(v, q.hi, v * q.lo); }
+__device__ __forceinline__ float2 over_scale2(float2 v, const RowScale& q) {
+  return fma2(v, splat2(q.hi), mul2(v, splat2(q.lo)));
+}
+
 template <int Q8>
 struct Code8;
 
 template <>
 struct Code8<FK_I8> {
   static constexpr float kMax = 127.0f;
-  // 1.5 * 2^23 + t has unit spacing, so the FMA rounds v * inv itself (the
-  // exact product) to the nearest integer, ties to even, and leaves it in
-  // two's complement in the low mantissa bits.
-  __device__ __forceinline__ static uint32_t one(float v, float inv) {
-    return __float_as_uint(fmaf(v, inv, 12582912.0f));
-  }
-  __device__ __forceinline__ static uint32_t pack4(const float* v, float inv) {
-    const float2 a = fma2(make_float2(v[0], v[1]), splat2(inv), splat2(12582912.0f));
-    const float2 b = fma2(make_float2(v[2], v[3]), splat2(inv), splat2(12582912.0f));
+  // 1.5 * 2^23 + t has unit spacing, so the sum rounds t to the nearest
+  // integer, ties to even, and leaves it in two's complement in the low
+  // mantissa bits.
+  static constexpr float kUnits = 12582912.0f;
+  __device__ __forceinline__ static uint32_t pack4(const float* v, const RowScale& q) {
+    const float2 a = add2(over_scale2(make_float2(v[0], v[1]), q), splat2(kUnits));
+    const float2 b = add2(over_scale2(make_float2(v[2], v[3]), q), splat2(kUnits));
     const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
     const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
   }
-  __device__ __forceinline__ static uint8_t pack1(float v, float inv) { return static_cast<uint8_t>(one(v, inv)); }
+  __device__ __forceinline__ static uint8_t pack1(float v, const RowScale& q) {
+    return static_cast<uint8_t>(__float_as_uint(over_scale(v, q) + kUnits));
+  }
 };
 
 template <>
@@ -65,28 +89,22 @@ struct Code8<FK_E4M3> {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
   }
-  __device__ __forceinline__ static uint32_t pack4(const float* v, float inv) {
-    const float2 a = mul2(make_float2(v[0], v[1]), splat2(inv)), b = mul2(make_float2(v[2], v[3]), splat2(inv));
+  __device__ __forceinline__ static uint32_t pack4(const float* v, const RowScale& q) {
+    const float2 a = over_scale2(make_float2(v[0], v[1]), q), b = over_scale2(make_float2(v[2], v[3]), q);
     return pair(a.x, a.y) | (static_cast<uint32_t>(pair(b.x, b.y)) << 16);
   }
-  __device__ __forceinline__ static uint8_t pack1(float v, float inv) {
-    return static_cast<uint8_t>(pair(v * inv, 0.0f));
+  __device__ __forceinline__ static uint8_t pack1(float v, const RowScale& q) {
+    return static_cast<uint8_t>(pair(over_scale(v, q), 0.0f));
   }
 };
 
-// What a row's codes are made with: scale is stored, inv multiplies the
-// values; a row that is not finite gets the scale NaN and codes 0 (`ok`).
-struct RowScale {
-  float scale, inv;
-  bool ok;
-};
 template <int Q8>
 __device__ __forceinline__ RowScale row_scale(float amax) {
   RowScale r;
   r.ok = amax <= 3.402823466e38f;  // neither NaN nor infinite
-  const float top = fmaxf(amax, kTinyAmax);
-  r.scale = r.ok ? __fdiv_rn(top, Code8<Q8>::kMax) : __int_as_float(0x7fffffff);
-  r.inv = __fdiv_rn(Code8<Q8>::kMax, top);
+  r.scale = r.ok ? fmaxf(amax, kTinyAmax) * (1.0f / Code8<Q8>::kMax) : __int_as_float(0x7fffffff);
+  r.hi = __frcp_rn(r.scale);
+  r.lo = r.hi * fmaf(-r.scale, r.hi, 1.0f);
   return r;
 }
 

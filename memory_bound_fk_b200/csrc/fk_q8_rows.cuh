@@ -143,7 +143,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, int c,
   uint8_t* const at = row + col_of_vec<VEC>(p, c);
   uint32_t w[W];
 #pragma unroll
-  for (int k = 0; k < W; ++k) w[k] = q.ok ? Code8<OUT>::pack4(v + 4 * k, q.inv) : 0u;
+  for (int k = 0; k < W; ++k) w[k] = q.ok ? Code8<OUT>::pack4(v + 4 * k, q) : 0u;
   if (!has_vec(p, c)) return;
   if constexpr (!ALIGNED)
     store_unaligned<W>(at, static_cast<int>(reinterpret_cast<uintptr_t>(at) & 3), w);

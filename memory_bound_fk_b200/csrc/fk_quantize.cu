@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_c
     if (t == 0 && cols > 0) a.scales[row] = q.scale;
 #pragma unroll
     for (int c = 0; c < VPT; ++c) store_codes<T, OUT, ALIGNED>(o, p, c, v + c * VEC, q);
-    if (!ALIGNED && edge >= 0) o[edge] = q.ok ? Code8<OUT>::pack1(ev, q.inv) : 0;
+    if (!ALIGNED && edge >= 0) o[edge] = q.ok ? Code8<OUT>::pack1(ev, q) : 0;
   });
 }
 
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(Quantiz
     const RowScale q = row_scale<OUT>(m);
     if (threadIdx.x == 0) a.scales[row] = q.scale;
     for (size_t j = threadIdx.x; j < cols; j += kStreamThreads)
-      o[j] = q.ok ? Code8<OUT>::pack1(act<EPI>(static_cast<float>(x[j])), q.inv) : 0;
+      o[j] = q.ok ? Code8<OUT>::pack1(act<EPI>(static_cast<float>(x[j])), q) : 0;
     __syncthreads();  // red is rewritten by the next row
   }
 }

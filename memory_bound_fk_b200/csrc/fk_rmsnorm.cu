@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
     }
     if (!ALIGNED && edge >= 0) {
       if constexpr (Q8)
-        (static_cast<uint8_t*>(a.y) + base)[edge] = q.ok ? Code8<OUT>::pack1(ev * rstd, q.inv) : 0;
+        (static_cast<uint8_t*>(a.y) + base)[edge] = q.ok ? Code8<OUT>::pack1(ev * rstd, q) : 0;
       else
         Elem<T>::store1(static_cast<T*>(a.y) + base + edge, ev * rstd);
     }
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kStreamThreads) rmsnorm_stream_kernel(RmsnormA
       }
       const float v = (a.gamma ? f * a.gamma[j] : f) * rstd;
       if constexpr (Q8) {
-        static_cast<uint8_t*>(a.y)[row * cols + j] = q.ok ? Code8<OUT>::pack1(v, q.inv) : 0;
+        static_cast<uint8_t*>(a.y)[row * cols + j] = q.ok ? Code8<OUT>::pack1(v, q) : 0;
       } else {
         static_cast<T*>(a.y)[row * cols + j] = static_cast<T>(v);
       }
