@@ -127,7 +127,8 @@ FK_API fk_status fk_rmsnorm_rows_bwd_ws(const void *dy, const void *h, const flo
  *   scales    [out] rows fp32 scales; must overlap neither.
  *   epilogue  an fk_epilogue: the values are quantised as they are, or
  *             through GELU in either form (computed in fp32, with the
- *             accuracy of fk_gelu on FK_F32).
+ *             accuracy of fk_gelu on FK_F32, and of negative values within
+ *             2^-14 relative as far down as a code of theirs is not 0).
  * The row is read once up to 131072 columns, twice beyond.
  * Weights [n, k] become per-channel scales by the same call.
  */

@@ -14,14 +14,16 @@ namespace {
 constexpr int kStreamThreads = 512;
 constexpr size_t kMaxGrid = 0x7fffffffu;
 
-// Inputs are raised to this first: GELU there is under 1e-21 (erf form) and
-// 1e-35 (tanh form), and what the two forms exponentiate stays in range.
-// Exact in bf16.
-constexpr float kActFloor = -9.875f;
-constexpr uint32_t kActFloorPair = 0xc11ec11eu;
+// Inputs are raised to kGeluFloor first, as in fk_gelu: both forms give -0
+// there, and -inf no longer meets inf * 0.  The floor has to lie where GELU is
+// 0 as fp32: a row of far negative values has a scale as small as its GELU, so
+// that no magnitude above 2^-119 (half a code of the smallest scale) is small
+// against it.  The tanh form's reciprocal flushes to 0 from -10 on, the erf
+// form's exponential from -13.1 on, GELU there being under 2^-122.
+constexpr uint32_t kGeluFloorPair = 0xc1f0c1f0u;  // two bf16 -30
 
 // GELU of a pair to fp32 accuracy, as gelu_tanh_f2 / gelu_erf_f2, of values
-// not below kActFloor.  (The reciprocal on the FMA pipes instead of MUFU,
+// not below kGeluFloor.  (The reciprocal on the FMA pipes instead of MUFU,
 // for all pairs or every other one: 46 and 39.6 us against 38.2 for
 // 16384 x 4096.)
 template <int EPI>
@@ -66,7 +68,7 @@ __device__ __forceinline__ float2 act2_joint(float2 x) {
 
 // A packed word's values raised to a floor (NaN stays), where GELU follows.
 template <typename T, int EPI>
-__device__ __forceinline__ uint4 raised(uint4 w, float floor = kActFloor, uint32_t floor_pair = kActFloorPair) {
+__device__ __forceinline__ uint4 raised(uint4 w, float floor = kGeluFloor, uint32_t floor_pair = kGeluFloorPair) {
   if constexpr (EPI != FK_EPILOGUE_NONE && sizeof(T) == 4) {
     w.x = __float_as_uint(max_nan(__uint_as_float(w.x), floor));
     w.y = __float_as_uint(max_nan(__uint_as_float(w.y), floor));
@@ -82,7 +84,7 @@ __device__ __forceinline__ uint4 raised(uint4 w, float floor = kActFloor, uint32
 }
 template <int EPI>
 __device__ __forceinline__ float act(float x) {
-  return act2<EPI>(splat2(EPI == FK_EPILOGUE_NONE ? x : max_nan(x, kActFloor))).x;
+  return act2<EPI>(splat2(EPI == FK_EPILOGUE_NONE ? x : max_nan(x, kGeluFloor))).x;
 }
 
 // The largest |GELU(x)| of negative x is 0.1701 (either form), and GELU rises
