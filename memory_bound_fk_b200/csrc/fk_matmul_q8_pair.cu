@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  cluster_sync();  // no arrival of either block is under way any more
+  cluster_sync();  // no arrival of either block is under way any more, and the other has read its accumulators
   if (warp == kEpiWarps + 1) tmem_dealloc_pair(tmem_slot, kTmemCols);
 }
 
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc::fence_before_sync();
-  __syncthreads();
+  cluster_sync();  // the pair frees its tensor memory together: the other block has read its half too
   if (warp == kEpiWarps + 1) tmem_dealloc_pair(tmem_slot, TOK);
 }
 

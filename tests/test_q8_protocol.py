@@ -1,0 +1,43 @@
+"""Order of steps in the kernels of the 8-bit layer that no run on a GPU shows
+reliably, read from their sources (without a GPU)."""
+import os
+import re
+
+import pytest
+
+import memory_bound_fk_b200
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(memory_bound_fk_b200.__file__)), "csrc")
+PRODUCT = ["fk_matmul_q8.cu", "fk_matmul_q8_pair.cu"]
+
+
+def text(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def kernels(name):
+    """(name, body) of each __global__ function of a source file."""
+    src, out = text(name), []
+    for m in re.finditer(r"__global__[^;{]*?\b(\w+_kernel)\s*\(", src):
+        at = src.index("{", m.end())
+        depth, end = 0, at
+        while True:
+            depth += {"{": 1, "}": -1}.get(src[end], 0)
+            end += 1
+            if depth == 0:
+                break
+        out.append((m.group(1), src[at:end]))
+    assert out
+    return out
+
+
+PRODUCT_KERNELS = [(f, k, b) for f in PRODUCT for k, b in kernels(f)]
+
+
+@pytest.mark.parametrize("file,kernel,body", PRODUCT_KERNELS, ids=[k for _, k, _ in PRODUCT_KERNELS])
+def test_a_pair_frees_its_tensor_memory_after_both_blocks_have_read_it(file, kernel, body):
+    if "tmem_dealloc_pair" not in body:
+        return
+    last_read = max(m.start() for m in re.finditer(r"tmem_ld\w+\(", body))
+    assert "cluster_sync();" in body[last_read:body.index("tmem_dealloc_pair")]
