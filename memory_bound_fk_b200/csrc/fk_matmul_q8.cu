@@ -80,7 +80,10 @@ __global__ void __launch_bounds__(kMmThreads)
   const int kb1 = static_cast<int>(static_cast<long long>(p.kblocks) * (part + 1) / SPLIT);
   volatile int* abort = &abort_flag;
 
-  if (warp == 5) tc::tmem_alloc(&tmem_slot, S::kTmemCols);
+  if (warp == 5) {
+    tc::tmem_alloc(&tmem_slot, S::kTmemCols);
+    let_next_start();
+  }
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
@@ -90,7 +93,6 @@ __global__ void __launch_bounds__(kMmThreads)
     abort_flag = 0;
     fence_mbarrier_init();
   }
-  let_next_start();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();

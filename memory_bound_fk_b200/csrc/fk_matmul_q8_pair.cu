@@ -89,9 +89,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbarrier_init();
   }
-  let_next_start();
   cluster_sync();  // every block's barriers stand
-  if (warp == kEpiWarps + 1) tmem_alloc_pair(&tmem_slot, kTmemCols);
+  if (warp == kEpiWarps + 1) {
+    tmem_alloc_pair(&tmem_slot, kTmemCols);
+    let_next_start();
+  }
   tc::fence_before_sync();
   cluster_arrive();  // the pair's tensor memory: waited for by all but the load warp, which does that at its end
   after_previous();
@@ -250,9 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbarrier_init();
   }
-  let_next_start();
   cluster_sync();  // every block's barriers stand
-  if (warp == kEpiWarps + 1) tmem_alloc_pair(&tmem_slot, TOK);
+  if (warp == kEpiWarps + 1) {
+    tmem_alloc_pair(&tmem_slot, TOK);
+    let_next_start();
+  }
   tc::fence_before_sync();
   cluster_arrive();  // the pairs' tensor memory, as in the persistent kernel
   after_previous();

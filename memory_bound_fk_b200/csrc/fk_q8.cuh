@@ -34,7 +34,11 @@ constexpr float kTinyAmax = 0x1p-100f;
 // (launch_overlapped) may start while its predecessor in the stream still
 // runs.  after_previous() returns once the predecessor has completed and its
 // writes are visible; nothing in global memory is touched before it.
-// let_next_start() allows the same to the successor.
+// let_next_start() allows the same to the successor, from the moment when one
+// thread of every block has called it (measured on B200: a block's first call
+// counts).  A kernel that takes tensor memory calls it from the warp that
+// allocates, after it has: otherwise the successor's blocks could hold the
+// columns, waiting for this kernel's end, that a block of it still waits for.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -41,3 +41,16 @@ def test_a_pair_frees_its_tensor_memory_after_both_blocks_have_read_it(file, ker
         return
     last_read = max(m.start() for m in re.finditer(r"tmem_ld\w+\(", body))
     assert "cluster_sync();" in body[last_read:body.index("tmem_dealloc_pair")]
+
+
+@pytest.mark.parametrize("file,kernel,body", PRODUCT_KERNELS, ids=[k for _, k, _ in PRODUCT_KERNELS])
+def test_the_next_kernel_may_start_once_tensor_memory_is_taken(file, kernel, body):
+    """A successor that starts early and takes tensor memory holds it until
+    this kernel has ended: no block of this one may still be waiting for any.
+    One thread's signal counts for its block, so it comes from the warp that
+    allocates."""
+    if "tmem_alloc" not in body:
+        assert "let_next_start();" in body
+        return
+    assert body.count("let_next_start();") == 1
+    assert re.search(r"if \(warp == [^)]*\) \{\s*(tc::)?tmem_alloc\w*\([^;]*\);\s*let_next_start\(\);\s*\}", body)
