@@ -160,8 +160,9 @@ FK_API fk_status fk_quantize_rows(const void *x, void *q, float *scales, size_t 
  * multiple of 128 is best: other pitches make TMA read across lines.)
  * Errors: FK_ERR_INVALID_ARG for a shape outside the above, bad pointers or
  * overlap; FK_ERR_UNSUPPORTED_DTYPE for another dtype or out_dtype.
- * A wait that gives up inside the kernel (see fk_wait_timeouts) leaves that
- * block of C unwritten.
+ * A wait that gives up inside the kernel (see fk_wait_timeouts; after 1 s, for
+ * a finished product 1 s and 2 us for each 128 codes of k) leaves that part of
+ * C unwritten.
  */
 FK_API fk_status fk_matmul_q8(const void *a, const void *b, const float *a_scales, const float *b_scales,
                               const float *bias, void *c, size_t m, size_t n, size_t k, int dtype, int out_dtype,
@@ -176,6 +177,13 @@ FK_API fk_status fk_matmul_q8_workspace(size_t m, size_t n, size_t k, int aligne
 FK_API fk_status fk_matmul_q8_ws(const void *a, const void *b, const float *a_scales, const float *b_scales,
                                  const float *bias, void *c, size_t m, size_t n, size_t k, int dtype, int out_dtype,
                                  int epilogue, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Self-test of the above: fk_matmul_q8 into fp32 whose waits for the finished
+ * product give up at once, each counted in fk_wait_timeouts.  C is left as it
+ * is; what runs inside the kernel ends before the kernel does. */
+FK_API fk_status fk_matmul_q8_wait_selftest(const void *a, const void *b, const float *a_scales,
+                                            const float *b_scales, float *c, size_t m, size_t n, size_t k, int dtype,
+                                            void *stream);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,7 @@ Raw C-ABI mirrors (same names, pointers as integers, stream as a
     fk_matmul_q8(a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, stream) -> status
     fk_matmul_q8_workspace(m, n, k, aligned) -> bytes
     fk_matmul_q8_ws(..., epilogue, workspace, workspace_bytes, stream) -> status
+    fk_matmul_q8_wait_selftest(a, b, a_scales, b_scales, c, m, n, k, dtype, stream) -> status
     fk_status_string(status) -> str
     fk_wait_timeouts(reset=False) -> int     (bounded-wait give-ups, synchronous)
     fk_wait_selftest(timeout_us, stream) -> status
@@ -173,6 +174,8 @@ def lib() -> ctypes.CDLL:
         L.fk_matmul_q8.restype = ci
         L.fk_matmul_q8_ws.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, sz, ci, ci, ci, vp, sz, vp]
         L.fk_matmul_q8_ws.restype = ci
+        L.fk_matmul_q8_wait_selftest.argtypes = [vp, vp, vp, vp, vp, sz, sz, sz, ci, vp]
+        L.fk_matmul_q8_wait_selftest.restype = ci
         L.fk_matmul_q8_workspace.argtypes = [sz, sz, sz, ci, szp]
         L.fk_matmul_q8_workspace.restype = ci
         L.fk_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint), ci]
@@ -324,6 +327,11 @@ def fk_matmul_q8_ws(a: int, b: int, a_scales: int, b_scales: int, bias: int, c: 
                     stream: int = 0) -> int:
     return lib().fk_matmul_q8_ws(a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, workspace,
                                  workspace_bytes, stream)
+
+
+def fk_matmul_q8_wait_selftest(a: int, b: int, a_scales: int, b_scales: int, c: int, m: int, n: int, k: int,
+                               dtype: int, stream: int = 0) -> int:
+    return lib().fk_matmul_q8_wait_selftest(a, b, a_scales, b_scales, c, m, n, k, dtype, stream)
 
 
 def fk_status_string(status: int) -> str:
@@ -815,5 +823,6 @@ __all__ = [
     "softmax_rows", "FK_I8", "FK_E4M3",
     "fk_rmsnorm_rows", "fk_rmsnorm_rows_bwd", "fk_rmsnorm_rows_bwd_workspace", "fk_rmsnorm_rows_bwd_ws",
     "fk_quantize_rows", "fk_matmul_q8", "fk_matmul_q8_workspace", "fk_matmul_q8_ws",
+    "fk_matmul_q8_wait_selftest",
     "rmsnorm", "rmsnorm_backward", "quantize_rows", "matmul_q8",
 ]

@@ -112,7 +112,11 @@ __global__ void __launch_bounds__(kMmThreads)
         tc::tma_load_2d(dst + kChan * kKBlock, &tma_a, &full[st], kb * kKBlock, m0);
       }
       // copies in flight land before the block exits (all have, unless a wait gave up)
-      for (int j = i > ST ? i - ST : 0; j < i; ++j) mm::drain(&full[j % ST], (j / ST) & 1);
+      for (int j = i > ST ? i - ST : 0; j < i; ++j)
+        if (!mm::drain(&full[j % ST], (j / ST) & 1)) {
+          *abort = 1;
+          break;
+        }
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -145,9 +149,13 @@ __global__ void __launch_bounds__(kMmThreads)
       bias = p.bias ? p.bias[chan] : 0.0f;
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");  // s_sa stands
-    mm::drain(&done, 0);
+    if (!mm::drain(&done, 0, p.done_ns)) {
+      *abort = 1;
+      mm::drain(&done, 0);  // MMAs that still run end before their memory goes
+    }
     tc::fence_after_sync();
   }
+  __syncthreads();  // one verdict for the block
   if constexpr (SPLIT > 1) cluster_wait();
   const bool good = *abort == 0;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kMmThreads)
     }
   } else {
     constexpr int OWN = TN / SPLIT;  // tokens this block finishes
-    if (warp < 4) {
+    if (warp < 4 && good) {
 #pragma unroll 1
       for (int t = 0; t < TN && m0 + t < p.m; t += 16) {
         uint32_t r[16];
@@ -292,9 +300,7 @@ cudaError_t launch_split(const mm::Call& c) {
   auto kernel = matmul_split_kernel<Q8, TN, SPLIT, T, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const mm::Params p = {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m),
-                        static_cast<int>(c.p.n), static_cast<int>((c.k + kKBlock - 1) / kKBlock),
-                        static_cast<int>(tiles_n), static_cast<int>(tiles_m)};
+  const mm::Params p = mm::make_params(c, tiles_n, tiles_m);
   return launch_overlapped(kernel, static_cast<unsigned>(tiles_n * tiles_m * SPLIT), kMmThreads, smem, SPLIT, c.stream,
                            ma, mb, p);
 }

@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_wait();
     // what was loaded has been read by the MMAs before the block exits
-    for (int j = i > kStages ? i - kStages : 0; j < i; ++j) drain(&empty[j % kStages], (j / kStages) & 1);
+    for (int j = i > kStages ? i - kStages : 0; j < i; ++j)
+      if (!drain(&empty[j % kStages], (j / kStages) & 1)) break;
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     // ---- MMAs, issued by the leader for both blocks
@@ -180,8 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = tl.m0 + half * (TOK / 2) + 32 * s + lane;
         sas[s] = tok < p.m ? __ldg(p.sa + tok) : 0.0f;
       }
-      const bool got = wait(&acc_full[buf], (u / 2) & 1, abort);
-      if (!__all_sync(0xffffffffu, got)) break;
+      const bool got = wait(&acc_full[buf], (u / 2) & 1, abort, p.done_ns);
+      if (!__all_sync(0xffffffffu, got)) {
+        // what may have been issued for this tile and the next ends before the block does
+        if (lane == 0 && drain(&acc_full[buf], (u / 2) & 1) && t + pairs < tiles)
+          drain(&acc_full[buf ^ 1], ((u + 1) / 2) & 1);
+        __syncwarp();
+        break;
+      }
       tc::fence_after_sync();
 #pragma unroll
       for (int s = 0; s < TOK / 2; s += 32) {
@@ -282,7 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_wait();
     // what was loaded has been read by the MMAs before the stages are used again
-    for (int j = i > kStages ? i - kStages : 0; j < i; ++j) drain(&empty[j % kStages], (j / kStages) & 1);
+    for (int j = i > kStages ? i - kStages : 0; j < i; ++j)
+      if (!drain(&empty[j % kStages], (j / kStages) & 1)) {
+        *abort = 1;
+        break;
+      }
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     cluster_wait();
@@ -314,15 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = tl.m0 + part * OWN + 32 * s + half * 16 + (lane & 15);
       sas[s] = tok < p.m ? __ldg(p.sa + tok) : 0.0f;
     }
-    drain(&done, 0);
+    if (!drain(&done, 0, p.done_ns)) {
+      *abort = 1;
+      drain(&done, 0);  // MMAs that still run end before their memory goes
+    }
     tc::fence_after_sync();
   }
-  __syncthreads();
+  __syncthreads();  // one verdict for the block
   if (tid < 2 * SPLIT) st_cluster(cluster_addr(&part_bad[rank], tid), *abort ? 1u : 0u);
-  cluster_sync();  // all MMAs of the cluster are done: the stages may be overwritten
+  cluster_sync();  // all MMAs of the cluster are done: the stages may be overwritten, unless a block gave up
+  bool good = true;
+#pragma unroll
+  for (int o = 0; o < 2 * SPLIT; ++o) good = good && part_bad[o] == 0;
 
   const uint32_t lane_base = tmem_slot + (static_cast<uint32_t>(quarter) << 21);
-  if (warp < kEpiWarps) {
+  if (warp < kEpiWarps && good) {
 #pragma unroll 1
     for (int t = half * (TOK / 2); t < (half + 1) * (TOK / 2) && tl.m0 + t < p.m; t += 16) {
       if (t / OWN == part) continue;  // OWN is a multiple of 16: a run of 16 has one owner
@@ -336,9 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   cluster_sync();  // every partial sum has arrived
   tc::fence_after_sync();
-  bool good = true;
-#pragma unroll
-  for (int o = 0; o < 2 * SPLIT; ++o) good = good && part_bad[o] == 0;
   if (warp < kEpiWarps && good) {
 #pragma unroll
     for (int i = 0; i < OWN / 32; ++i) {
@@ -403,9 +417,7 @@ cudaError_t launch_shape(const Call& c) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Shape<TOK>::kSmem));
   if (e != cudaSuccess) return e;
-  const Params p = {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m), static_cast<int>(c.p.n),
-                    static_cast<int>((c.k + kKBlock - 1) / kKBlock), static_cast<int>(tiles_n),
-                    static_cast<int>(tiles_m)};
+  const Params p = make_params(c, tiles_n, tiles_m);
   const size_t pairs = static_cast<size_t>(c.sm_count) / 2, tiles = tiles_n * tiles_m;
   return launch_overlapped(kernel, static_cast<unsigned>(SPLIT > 0 ? 2 * SPLIT * tiles : 2 * (tiles < pairs ? tiles : pairs)),
                            kThreads, Shape<TOK>::kSmem, SPLIT > 0 ? 2 * SPLIT : 2, c.stream, ma, mb, p);

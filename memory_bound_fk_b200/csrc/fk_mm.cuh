@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "fk_gelu.cuh"
+#include "fk_mm_host.h"
 #include "fk_q8.h"
 #include "fk_sync.cuh"
 #include "fk_tc.cuh"
@@ -15,34 +16,36 @@ namespace mm {
 
 // Threads of this source file's kernels whose bounded wait gave up.
 static __device__ unsigned g_mm_wait_timeouts;
-constexpr uint64_t kWaitNs = 1000000000ull;
 
-// Bounded mbarrier wait: gives up after 1 s, is counted, and raises the
-// block's abort flag, on which its other waits return at once.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (;;) {
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;  // suspended up to 20 us per try
-    if (*abort) return false;
-    if (global_ns() - t0 > kWaitNs) {
-      atomicAdd(&g_mm_wait_timeouts, 1u);
-      *abort = 1;
-      return false;
-    }
+// Bounded mbarrier wait: gives up after `limit` (0: at once, for the
+// self-test), is counted, and raises the block's abort flag, on which its
+// other waits return at once.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit = kWaitNs) {
+  if (limit != 0) {
+    if (mbar_test_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    do {
+      if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;  // suspended up to 20 us per try
+      if (*abort) return false;
+    } while (global_ns() - t0 <= limit);
   }
+  atomicAdd(&g_mm_wait_timeouts, 1u);
+  *abort = 1;
+  return false;
 }
 
 // Bounded wait that ignores the abort flag: copies and MMAs in flight land
-// before the block goes on to exit.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-    if (global_ns() - t0 > kWaitNs) {
-      atomicAdd(&g_mm_wait_timeouts, 1u);
-      return;
-    }
+// before the block goes on.  False if it gave up: then they may still run, and
+// the caller raises the abort flag.
+__device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity, uint64_t limit = kWaitNs) {
+  if (limit != 0) {
+    const uint64_t t0 = global_ns();
+    do {
+      if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    } while (global_ns() - t0 <= limit);
   }
+  atomicAdd(&g_mm_wait_timeouts, 1u);
+  return false;
 }
 
 // Instruction descriptor of a dense 8-bit MMA, both operands K-major, M x N:

@@ -12,6 +12,11 @@ namespace mm {
 
 constexpr int kKBlock = 128;  // codes of k per stage (one swizzled row)
 
+// Limits of the kernels' waits, ns: for a stage or an accumulator; and what the
+// wait for a finished product has more for each 128-code step of k (a step
+// takes 0.3 us alone).
+constexpr uint64_t kWaitNs = 1000000000ull, kStepNs = 2000;
+
 struct Params {
   const float* sa;
   const float* sb;
@@ -20,6 +25,7 @@ struct Params {
   int m, n;
   int kblocks;  // ceil(k / 128)
   int tiles_n, tiles_m;
+  uint64_t done_ns;  // limit of the wait for a finished product
 };
 
 // A product whose operands TMA can read: [m, k] and [n, k] with row pitches
@@ -31,6 +37,13 @@ struct Call {
   int sm_count;
   cudaStream_t stream;
 };
+
+inline Params make_params(const Call& c, size_t tiles_n, size_t tiles_m) {
+  const size_t kblocks = (c.k + kKBlock - 1) / kKBlock;
+  return {c.p.a_scales, c.p.b_scales, c.p.bias, c.p.c, static_cast<int>(c.p.m), static_cast<int>(c.p.n),
+          static_cast<int>(kblocks), static_cast<int>(tiles_n), static_cast<int>(tiles_m),
+          c.p.give_up ? 0 : kWaitNs + kStepNs * kblocks};
+}
 
 // [rows, k] codes in boxes of 128 codes x box_rows rows, 128-byte swizzle;
 // outside reads 0.

@@ -138,7 +138,7 @@ fk_status rmsnorm_bwd_call(const void* dy, const void* h, const float* gamma, co
 
 fk_status matmul_call(const void* a, const void* b, const float* a_scales, const float* b_scales, const float* bias,
                       void* c, size_t m, size_t n, size_t k, int dtype, int out_dtype, int epilogue, void* ws,
-                      size_t ws_bytes, bool own, void* stream) {
+                      size_t ws_bytes, bool own, void* stream, bool give_up = false) {
   if (!q8_dtype(dtype) || !float_dtype(out_dtype)) return FK_ERR_UNSUPPORTED_DTYPE;
   if (!known_epilogue(epilogue)) return FK_ERR_INVALID_ARG;
   if (m == 0 || n == 0) return FK_OK;
@@ -157,7 +157,7 @@ fk_status matmul_call(const void* a, const void* b, const float* a_scales, const
   if (st != FK_OK) return st;
   const DeviceInfo* dev = current_device_info(nullptr);
   if (dev == nullptr) return FK_ERR_UNSUPPORTED_DEVICE;
-  const MatmulQ8Args args = {a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue};
+  const MatmulQ8Args args = {a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, give_up};
   const size_t need = matmul_q8_workspace(m, n, k, aligned16(a) && aligned16(b));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return with_workspace(need, ws, ws_bytes, own, sp, 6, s,
@@ -251,6 +251,12 @@ fk_status fk_matmul_q8_ws(const void* a, const void* b, const float* a_scales, c
                           int epilogue, void* workspace, size_t workspace_bytes, void* stream) {
   return fk::matmul_call(a, b, a_scales, b_scales, bias, c, m, n, k, dtype, out_dtype, epilogue, workspace,
                          workspace_bytes, false, stream);
+}
+
+fk_status fk_matmul_q8_wait_selftest(const void* a, const void* b, const float* a_scales, const float* b_scales,
+                                     float* c, size_t m, size_t n, size_t k, int dtype, void* stream) {
+  return fk::matmul_call(a, b, a_scales, b_scales, nullptr, c, m, n, k, dtype, FK_F32, FK_EPILOGUE_NONE, nullptr, 0,
+                         true, stream, true);
 }
 
 fk_status fk_matmul_q8_workspace(size_t m, size_t n, size_t k, int aligned, size_t* bytes) {

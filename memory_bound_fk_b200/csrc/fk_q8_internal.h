@@ -99,6 +99,7 @@ struct MatmulQ8Args {
   void* c;
   size_t m, n, k;
   int dtype, out_dtype, epilogue;
+  bool give_up;  // self-test: the wait for the finished product gives up at once
 };
 // `aligned`: a and b on 16-byte boundaries.
 size_t matmul_q8_workspace(size_t m, size_t n, size_t k, bool aligned);
