@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(256)
       const uint32_t* q = reinterpret_cast<const uint32_t*>(src + at - shift);
       uint32_t v[5];
 #pragma unroll
-      for (int j = 0; j < 5; ++j) v[j] = __ldg(q + j);
+      for (int j = 0; j < 5; ++j) v[j] = q[j];
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], static_cast<unsigned>(shift) * 8);
     } else {

@@ -172,14 +172,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = u & 1;
       const int chan = tl.n0 + rank * kChan + quarter * 32 + lane;
       const bool in = chan < p.n;
-      const float sb = in ? __ldg(p.sb + chan) : 0.0f;
-      const float bias = in && p.bias ? __ldg(p.bias + chan) : 0.0f;
+      const float sb = in ? ld_param(p.sb + chan) : 0.0f;
+      const float bias = in && p.bias ? ld_param(p.bias + chan) : 0.0f;
       // this warp's token scales, one token of each 32 per lane, fetched before the wait
       float sas[TOK / 64];
 #pragma unroll
       for (int s = 0; s < TOK / 64; ++s) {
         const int tok = tl.m0 + half * (TOK / 2) + 32 * s + lane;
-        sas[s] = tok < p.m ? __ldg(p.sa + tok) : 0.0f;
+        sas[s] = tok < p.m ? ld_param(p.sa + tok) : 0.0f;
       }
       const bool got = wait(&acc_full[buf], (u / 2) & 1, abort, p.done_ns);
       if (!__all_sync(0xffffffffu, got)) {
@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     cluster_wait();
-    sb = in ? __ldg(p.sb + chan) : 0.0f;
-    bias = in && p.bias ? __ldg(p.bias + chan) : 0.0f;
+    sb = in ? ld_param(p.sb + chan) : 0.0f;
+    bias = in && p.bias ? ld_param(p.bias + chan) : 0.0f;
 #pragma unroll
     for (int s = 0; s < OWN / 32; ++s) {
       const int tok = tl.m0 + part * OWN + 32 * s + half * 16 + (lane & 15);
-      sas[s] = tok < p.m ? __ldg(p.sa + tok) : 0.0f;
+      sas[s] = tok < p.m ? ld_param(p.sa + tok) : 0.0f;
     }
     if (!drain(&done, 0, p.done_ns)) {
       *abort = 1;

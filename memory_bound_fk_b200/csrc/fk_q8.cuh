@@ -42,6 +42,32 @@ constexpr float kTinyAmax = 0x1p-100f;
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What a kernel launched this way reads with, in place of __ldg and the
+// non-coherent loads of fk_common.cuh: their data must not change while the
+// kernel lives, and the predecessor may still be writing it when this one
+// starts.
+__device__ __forceinline__ float ld_param(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_param4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+// 16 bytes of a row that is read once, zeros when !pred (nothing is read then).
+__device__ __forceinline__ uint4 ld_row_v4_if(const void* p, bool pred) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"(static_cast<unsigned>(pred))
+      : "memory");
+  return v;
+}
+
 // max(a, |b|), NaN if either is.
 __device__ __forceinline__ float absmax_nan(float a, float b) {
   float r;

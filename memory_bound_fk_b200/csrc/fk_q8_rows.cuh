@@ -68,13 +68,13 @@ __device__ __forceinline__ int edge_col(const Place& p) {
   return p.t < p.cols - in ? (p.t < p.head ? p.t : in + p.t) : -1;
 }
 
-// The thread's VPT vectors of a row, as packed 16-byte words; zeros where
-// there is none.
+// VPT of the thread's vectors of a row, the first of them its vector `from`,
+// as packed 16-byte words; zeros where there is none.
 template <typename T, int VPT>
-__device__ __forceinline__ void load_vecs(const T* row, const Place& p, uint4* raw) {
+__device__ __forceinline__ void load_vecs(const T* row, const Place& p, uint4* raw, int from = 0) {
 #pragma unroll
   for (int c = 0; c < VPT; ++c)
-    raw[c] = ld_stream_v4_if(row + col_of_vec<Elem<T>::VEC>(p, c), has_vec(p, c), 0u);
+    raw[c] = ld_row_v4_if(row + col_of_vec<Elem<T>::VEC>(p, from + c), has_vec(p, from + c));
 }
 
 // One value of the rows' type, and the rounding to it.
@@ -170,11 +170,11 @@ __device__ __forceinline__ void load_params(const float* g, const Place& p, int 
     float4 z = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
     const int i = from + k;
     if (ALIGNED || i + 4 <= p.cols) {
-      z = __ldg(reinterpret_cast<const float4*>(g + i));
+      z = ld_param4(g + i);
     } else if (i < p.cols) {
-      z.x = __ldg(g + i);
-      if (i + 1 < p.cols) z.y = __ldg(g + i + 1);
-      if (i + 2 < p.cols) z.z = __ldg(g + i + 2);
+      z.x = ld_param(g + i);
+      if (i + 1 < p.cols) z.y = ld_param(g + i + 1);
+      if (i + 2 < p.cols) z.z = ld_param(g + i + 2);
     }
     a[k] = z.x;
     a[k + 1] = z.y;

@@ -48,18 +48,24 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
     float ev = 0.0f, er = 0.0f;  // this thread's value outside the vectors
     if (!ALIGNED && edge >= 0) ev = load_one(x + edge);
     if (a.residual) {
-      uint4 add[VPT];
-      load_vecs<T, VPT>(res, p, add);
+      // at most 16 fp32 values of the residual at a time: with all 32 beside
+      // those of x a thread spills
+      constexpr int PART = sizeof(T) == 4 && EPT == 32 ? VPT / 2 : VPT;
       if (!ALIGNED && edge >= 0) er = load_one(res + edge);
 #pragma unroll
-      for (int c = 0; c < VPT; ++c) {
-        float f[VEC], r[VEC];
-        Elem<T>::unpack(raw[c], f);
-        Elem<T>::unpack(add[c], r);
+      for (int from = 0; from < VPT; from += PART) {
+        uint4 add[PART];
+        load_vecs<T, PART>(res, p, add, from);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] += r[k];
-        raw[c] = Elem<T>::pack(f);  // h, rounded to the rows' type: what is normalised is what is stored
-        if (a.h) store_vec(h, p, c, raw[c]);
+        for (int c = from; c < from + PART; ++c) {
+          float f[VEC], r[VEC];
+          Elem<T>::unpack(raw[c], f);
+          Elem<T>::unpack(add[c - from], r);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) f[k] += r[k];
+          raw[c] = Elem<T>::pack(f);  // h, rounded to the rows' type: what is normalised is what is stored
+          if (a.h) store_vec(h, p, c, raw[c]);
+        }
       }
       if (!ALIGNED && edge >= 0) {
         ev = round_one<T>(ev + er);
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
     }
     if (!ALIGNED && edge >= 0) {
       s = fmaf(ev, ev, s);
-      if (a.gamma) ev *= __ldg(a.gamma + edge);
+      if (a.gamma) ev *= ld_param(a.gamma + edge);
       if (Q8) m = absmax_nan(m, ev);
     }
     if constexpr (CL > 1)

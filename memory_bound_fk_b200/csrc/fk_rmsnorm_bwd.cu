@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, EPT == 32 ? 1 : EPT == 16 ? 2 
   after_previous();
   float gam[EPT], acc[EPT];
   float eg = 1.0f, ea = 0.0f, eh = 0.0f, ed = 0.0f;  // gamma, sum, h and dy of this thread's column outside the vectors
-  if (!ALIGNED && edge >= 0 && a.gamma) eg = __ldg(a.gamma + edge);
+  if (!ALIGNED && edge >= 0 && a.gamma) eg = ld_param(a.gamma + edge);
 #pragma unroll
   for (int c = 0; c < VPT; ++c) load_params<VEC, ALIGNED>(a.gamma, p, c, gam + c * VEC);
 #pragma unroll
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float gam[EPT], acc[EPT];
   float eg = 1.0f, ea = 0.0f, eh = 0.0f, ed = 0.0f;  // gamma, sum, h and dy of this thread's column outside the vectors
   if (!ALIGNED && edge >= 0) {
-    if (a.gamma) eg = __ldg(a.gamma + edge);
+    if (a.gamma) eg = ld_param(a.gamma + edge);
     if (team < a.rows) {
       eh = load_one(h + team * a.cols + edge);
       ed = load_one(dy + team * a.cols + edge);

@@ -54,3 +54,25 @@ def test_the_next_kernel_may_start_once_tensor_memory_is_taken(file, kernel, bod
         return
     assert body.count("let_next_start();") == 1
     assert re.search(r"if \(warp == [^)]*\) \{\s*(tc::)?tmem_alloc\w*\([^;]*\);\s*let_next_start\(\);\s*\}", body)
+
+
+def test_early_started_kernels_read_coherently():
+    """A kernel that starts while its predecessor writes may not read that
+    data as constant for its life (non-coherent loads, __ldg, which the
+    compiler may also move ahead of the wait)."""
+    for name in sorted(os.listdir(CSRC)):
+        src = text(name)
+        if "after_previous()" in src or name == "fk_q8_rows.cuh":
+            for banned in ("__ldg", ".nc.", "ld_stream_v4", "load1(", "__restrict__"):
+                assert banned not in src, f"{banned} in {name}"
+
+
+def test_every_early_started_kernel_waits_for_its_predecessor():
+    seen = 0
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith(".cu") and "launch_overlapped(" in text(name):
+            for kernel, body in kernels(name):
+                if "let_next_start();" in body:
+                    assert body.count("after_previous();") == 1
+                    seen += 1
+    assert seen >= 9
