@@ -170,12 +170,15 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_c
 
 // Wide bf16 rows: blocks that stay and walk the rows, the next row loaded
 // before the current one is computed.  Measured on B200 (8192 x 16384 to
-// e4m3): 63 us plain (6.4 TB/s), 80 through the tanh form (93 with a
-// reciprocal for each value, one read a warp of the row's maxima and the
-// scale applied to single values), 137 through the erf form (25 instructions
-// a value: issue).  The tanh form's rest: MUFU, with 1.5 operations a value
-// at least 46 us, and issue, at 15 instructions a value 57, in turns between
-// barriers.
+// e4m3): 63 us plain (6.4 TB/s), 82 through the tanh form (with the quotient
+// left unrounded, v (Q / max), 80; and 93 with a reciprocal for each value,
+// one read a warp of the row's maxima and the scale applied to single values),
+// 138 through the erf form (26 instructions a value: issue).  The tanh form's
+// rest: MUFU, with 1.5 operations a value at least 46 us, and issue, at 16
+// instructions a value 60, in turns between barriers.
+// Rows whose largest value does not decide the scale (all below about 0.28)
+// take GELU of their packed values twice: 159 and 230 us (rows of 0.05
+// deviation; 553 and 617 when they were read again, value by value).
 // Rows of up to 8192 columns do not gain (4096: 38.4 against 37.5 with one
 // row per block), nor do shifted ones (16383: 112 against 96).
 template <typename T, int OUT, int EPI, int EPT, int MAXT, int MINB>
@@ -216,8 +219,16 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_
       rises = m > kGeluDip;
       if (!rises) {  // small or negative values only, or a NaN: the same for the whole block
         m = 0.0f;
-#pragma unroll 1
-        for (int j = t; j < cols; j += team) m = absmax_nan(m, act<EPI>(static_cast<float>(x[base + j])));
+#pragma unroll
+        for (int c = 0; c < VPT; ++c) {
+          float f[VEC];
+          Elem<T>::unpack(raised<T, EPI>(raw[c]), f);
+#pragma unroll
+          for (int k = 0; k < VEC; k += 2) {
+            const float2 z = act2<EPI>(make_float2(f[k], f[k + 1]));
+            m = absmax_nan(absmax_nan(m, z.x), z.y);
+          }
+        }
         team_max<0>(m, dip);
         __syncthreads();  // dip may be used by the next row
       }

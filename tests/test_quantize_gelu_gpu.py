@@ -74,3 +74,50 @@ def test_rows_far_below_zero(fk, torch_mod, cols, off, dtype, gelu):
         c, s = got = run(fk, torch, x, kind, gelu, off)
         check(x, kind, gelu, got)
         assert np.all(c[10:] == 0) and np.all(s[10:] == np.float32(2.0 ** -100) * (np.float32(1) / np.float32(q8.QMAX[kind])))
+
+
+@pytest.mark.parametrize("gelu", ["tanh", "erf"])
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("rows,cols", [(700, 8200), (1000, 8704), (640, 12000), (450, 16384), (2000, 16376)])
+def test_wide_rows_of_both_kinds_in_turn(fk, torch_mod, rows, cols, kind, gelu):
+    """More rows than blocks stay resident, so that each block walks several:
+    rows whose scale their largest value decides, rows of small or negative
+    values only, NaN, zeros and far values follow each other in every order."""
+    torch = torch_mod
+    g = np.random.default_rng(rows)
+    x = make_rows(rows, cols, "f32", cols)
+    sort = g.integers(0, 8, rows)
+    for i in np.nonzero(sort == 1)[0]:
+        x[i] *= 0.01                                       # all below the dip
+    for i in np.nonzero(sort == 2)[0]:
+        x[i] = -x[i].abs() - 0.01                          # all negative
+    for i in np.nonzero(sort == 3)[0]:
+        x[i, int(g.integers(cols))] = float("nan")
+    for i in np.nonzero(sort == 4)[0]:
+        x[i] = x[i].clamp(-3.0, 0.2)
+        x[i, int(g.integers(cols))] = -0.75                # the dip, in one place
+    for i in np.nonzero(sort == 5)[0]:
+        x[i] = 0.0 if i % 3 else -25.0
+    for i in np.nonzero(sort == 6)[0]:
+        x[i, int(g.integers(cols))] = 1.0e30 if i % 2 else float("inf")
+    x = x.bfloat16()
+    check_rows = np.unique(np.concatenate([g.integers(0, rows, 60), [0, 1, rows - 2, rows - 1]]))
+    c, s = run(fk, torch, x, kind, gelu)
+    check(x[check_rows], kind, gelu, (c[check_rows], s[check_rows]))
+    # a row's codes do not depend on its place: every row again, in reverse
+    c2, s2 = run(fk, torch, x.flip(0).contiguous(), kind, gelu)
+    assert np.array_equal(c, c2[::-1]) and np.array_equal(s, s2[::-1], equal_nan=True)
+
+
+@pytest.mark.parametrize("gelu", [None, "tanh", "erf"])
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+def test_wide_rows_one_by_one_and_together(fk, torch_mod, kind, gelu):
+    """Rows of a long matrix get the codes that each gets alone."""
+    torch = torch_mod
+    x = make_rows(1500, 9216, "bf16", 4).cuda()
+    x[::7] *= 0.02
+    dt = torch.int8 if kind == "i8" else torch.float8_e4m3fn
+    q, s = fk.quantize_rows(x, dt, gelu=gelu)
+    for i in list(range(0, 1500, 97)) + [295, 296, 297, 443, 444, 445, 1499]:
+        q1, s1 = fk.quantize_rows(x[i:i + 1].contiguous(), dt, gelu=gelu)
+        assert torch.equal(q[i].view(torch.uint8), q1[0].view(torch.uint8)) and torch.equal(s[i], s1[0])
