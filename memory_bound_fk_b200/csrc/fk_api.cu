@@ -44,14 +44,19 @@ cudaMemPool_t workspace_pool(int dev) {
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
+    // the first call may stand in a stream capture, which making a pool would
+    // end in this thread's default mode; the pool is no part of the capture
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     cudaMemPool_t pool = nullptr;
-    if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) {
+    if (cudaMemPoolCreate(&pool, &props) == cudaSuccess) {
+      uint64_t keep = uint64_t{64} << 20;
+      (void)cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+      g_pool[dev] = pool;
+    } else {
       (void)cudaGetLastError();
-      return;
     }
-    uint64_t keep = uint64_t{64} << 20;
-    (void)cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    g_pool[dev] = pool;
+    if (relaxed) (void)cudaThreadExchangeStreamCaptureMode(&mode);
   });
   return g_pool[dev];
 }
