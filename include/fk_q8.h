@@ -17,10 +17,13 @@
  *   rmsnorm (8 bits) -> matmul_q8 -> quantize_rows (GELU) -> matmul_q8.
  *
  * fk.h's conventions on memory, streams, errors, devices and threads hold
- * here too.  Workspace: fk_rmsnorm_rows_bwd (when dgamma is asked for) and
- * fk_matmul_q8 (when k is not a multiple of 16, or a or b is not 16-byte
- * aligned) take theirs stream-ordered from the library's private pool; the
- * _ws forms take the caller's and allocate nothing.
+ * here too.  Workspace: fk_rmsnorm_rows_bwd (when dgamma is asked for, and for
+ * rows that are read value by value, see there) and fk_matmul_q8 (when k is
+ * not a multiple of 16, or a or b is not 16-byte aligned: up to (m + n) rows of
+ * k codes) take theirs stream-ordered from the library's private pool.  The
+ * pool keeps 64 MiB; a larger workspace is mapped anew after each
+ * synchronisation, and better given by the caller: the _ws forms take the
+ * caller's and allocate nothing.
  *
  * Eight-bit rows.  A row v of fp32 values becomes codes and one fp32 scale:
  *     scale = max(max_j |v_j|, 2^-100) / Q,   code_j = round(v_j / scale),
@@ -69,7 +72,9 @@ typedef enum fk_q8type {
  * elsewhere.  Every other overlap of an output with an input or another
  * output is rejected.
  * Arithmetic in fp32.  The row is read once up to 131072 columns; longer rows
- * are read twice.  A row whose h holds a NaN or an infinity, or whose sum of
+ * are read twice, value by value, as are rows of buffers that lie differently:
+ * x, residual, h (and y in the rows' type) at different offsets from a 16-byte
+ * boundary, or gamma off one.  A row whose h holds a NaN or an infinity, or whose sum of
  * squares overflows fp32 (|h| past about 1e19), is NaN throughout (8-bit:
  * scale NaN, codes 0).  eps == 0 makes a row of zeros NaN, and a row of
  * values whose squares underflow (below about 1e-22) counts as one.  The
@@ -99,8 +104,10 @@ FK_API fk_status fk_rmsnorm_rows(const void *x, const void *residual, const floa
  *   dgamma [out] cols fp32 values, or NULL (not computed).  rows == 0 gives 0.
  *   eps    as in the forward call.
  * Arithmetic in fp32; dgamma is summed in fp32 in an order fixed by the
- * shape (two equal calls give equal bits).  Rows up to 65536 columns are
- * read once.
+ * shape and the way the buffers lie (two equal calls give equal bits).  Rows
+ * up to 65536 columns are read once.  Longer ones, and rows of buffers that lie
+ * differently (dy, h, dres and dx at different offsets from a 16-byte boundary,
+ * or gamma off one), are read value by value, dy and h three times.
  * Errors as fk_rmsnorm_rows; dgamma must overlap nothing.
  */
 FK_API fk_status fk_rmsnorm_rows_bwd(const void *dy, const void *h, const float *gamma, const void *dres, void *dx,

@@ -131,7 +131,9 @@ fk_status rmsnorm_bwd_call(const void* dy, const void* h, const float* gamma, co
   if (st != FK_OK) return st;
   const RmsnormBwdArgs a = {dy, h, gamma, dres, dx, dgamma, rows, cols, dtype, eps,
                             row_mode(cols * es, {dy, h, dres, dx}, gamma, nullptr)};
-  const size_t need = rmsnorm_bwd_workspace(rows, cols, dtype, dgamma != nullptr);
+  // the library takes what this call uses; a caller's is as large as any call of the shape may need
+  const size_t need = own ? rmsnorm_bwd_workspace(rows, cols, dtype, dgamma != nullptr, a.mode)
+                          : rmsnorm_bwd_workspace(rows, cols, dtype, dgamma != nullptr);
   return with_workspace(need, ws, ws_bytes, own, sp, 6, s,
                         [&](void* w) { return launch_rmsnorm_bwd(a, w, s); });
 }

@@ -75,7 +75,8 @@ struct RmsnormBwdArgs {
   float eps;
   RowMode mode;
 };
-size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma);
+size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma, RowMode mode);
+size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma);  // the most of any mode
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, void* ws, cudaStream_t stream);
 
 // ---- rows to 8 bits ----------------------------------------------------------

@@ -570,15 +570,21 @@ cudaError_t launch_type(const RmsnormBwdArgs& a, void* ws, cudaStream_t s) {
 
 }  // namespace
 
+// What the kernels of this way of lying use.
+size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma, RowMode mode) {
+  if (mode == kRowsAny || cols > kBwdMaxCols)
+    return stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
+  return want_dgamma ? bwd_launch(rows, cols, vec_elems(dtype), mode != kRowsAligned).groups * cols * sizeof(float) : 0;
+}
+
 // Enough for every way the buffers may lie.
 size_t rmsnorm_bwd_workspace(size_t rows, size_t cols, int dtype, bool want_dgamma) {
-  const size_t stream = stats_bytes(rows) + (want_dgamma ? stream_groups(rows) * cols * sizeof(float) : 0);
-  if (cols > kBwdMaxCols || !want_dgamma) return stream;
-  size_t groups = bwd_launch(rows, cols, vec_elems(dtype), false).groups;
-  const size_t shifted = bwd_launch(rows, cols, vec_elems(dtype), true).groups;
-  if (shifted > groups) groups = shifted;
-  const size_t rowed = groups * cols * sizeof(float);
-  return rowed > stream ? rowed : stream;
+  size_t most = 0;
+  for (RowMode mode : {kRowsAligned, kRowsShifted, kRowsAny}) {
+    const size_t need = rmsnorm_bwd_workspace(rows, cols, dtype, want_dgamma, mode);
+    most = need > most ? need : most;
+  }
+  return most;
 }
 
 cudaError_t launch_rmsnorm_bwd(const RmsnormBwdArgs& a, void* ws, cudaStream_t stream) {
