@@ -196,8 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tok >= p.m) break;
         const float sa = sas[s / 32];
         uint32_t r[32];
-        tc::tmem_ld32_async(lane_base + buf * TOK + col, r);
-        tc::tmem_wait_ld();
+        tmem_ld32(lane_base + buf * TOK + col, r);
         T* out = c + static_cast<size_t>(tok) * p.n + chan;
         const int left = p.m - tok;
 #pragma unroll

@@ -76,3 +76,12 @@ def test_every_early_started_kernel_waits_for_its_predecessor():
                     assert body.count("after_previous();") == 1
                     seen += 1
     assert seen >= 9
+
+
+def test_accumulators_are_used_after_the_wait_for_their_load():
+    """A tcgen05.ld fills its registers later: in one asm statement with its
+    wait, no use of them can be placed between the two."""
+    for name in PRODUCT:
+        assert "tmem_ld32_async" not in text(name)
+    for m in re.finditer(r"__device__[^{]*\btmem_ld\w*\([^{]*\{(.*?)\n\}", text("fk_mm.cuh"), re.S):
+        assert m.group(1).count("asm volatile") == 1 and "tcgen05.wait::ld" in m.group(1)
