@@ -70,11 +70,11 @@ __device__ __forceinline__ int edge_col(const Place& p) {
 
 // VPT of the thread's vectors of a row, the first of them its vector `from`,
 // as packed 16-byte words; zeros where there is none.
-template <typename T, int VPT>
+template <typename T, int VPT, bool RELAXED = false>
 __device__ __forceinline__ void load_vecs(const T* row, const Place& p, uint4* raw, int from = 0) {
 #pragma unroll
   for (int c = 0; c < VPT; ++c)
-    raw[c] = ld_row_v4_if(row + col_of_vec<Elem<T>::VEC>(p, from + c), has_vec(p, from + c));
+    raw[c] = ld_row_v4_if<RELAXED>(row + col_of_vec<Elem<T>::VEC>(p, from + c), has_vec(p, from + c));
 }
 
 // One value of the rows' type, and the rounding to it.

@@ -32,6 +32,7 @@ template <typename T, int OUT, int EPT, bool ALIGNED, int LANES, int MAXT, int M
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_constant__ RmsnormArgs a) {
   constexpr bool Q8 = OUT == FK_I8 || OUT == FK_E4M3;
   constexpr int VEC = Elem<T>::VEC, VPT = EPT / VEC;
+  constexpr bool RELAXED = CL > 1 && sizeof(T) == 2;
   __shared__ float2 red[LANES ? 1 : CL * (MAXT / 32)];
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   let_next_start();
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
     const Place p = place_of<T, ALIGNED>(t, team, cols, x);
     const int edge = ALIGNED ? -1 : edge_col<VEC>(p);
     uint4 raw[VPT];
-    load_vecs<T, VPT>(x, p, raw);
+    load_vecs<T, VPT, RELAXED>(x, p, raw);
     float ev = 0.0f, er = 0.0f;  // this thread's value outside the vectors
     if (!ALIGNED && edge >= 0) ev = load_one(x + edge);
     if (a.residual) {
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_row_kernel(const __grid_co
 #pragma unroll
       for (int from = 0; from < VPT; from += PART) {
         uint4 add[PART];
-        load_vecs<T, PART>(res, p, add, from);
+        load_vecs<T, PART, RELAXED>(res, p, add, from);
 #pragma unroll
         for (int c = from; c < from + PART; ++c) {
           float f[VEC], r[VEC];
