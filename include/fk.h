@@ -29,13 +29,16 @@
  *            device can access (cudaMalloc / torch tensors, managed or
  *            mapped pinned host memory).  Pageable host memory is rejected
  *            (FK_ERR_INVALID_ARG).  libfk holds no handles and keeps no state
- *            besides a per-device properties cache.  The only allocation it
- *            ever makes is the workspace of the split path (FK_PATH_SPLIT:
- *            very long rows, few of them), a few KiB to at most 8 MiB taken
- *            stream-ordered on the caller's stream from a private memory pool
- *            of the library (which keeps up to 64 MiB reserved between calls)
- *            and released on the same stream; fk_softmax_rows_ws takes a
- *            caller-provided workspace instead and allocates nothing.
+ *            besides a per-device properties cache and memory pool.  The only
+ *            allocations it makes are workspaces, taken stream-ordered on the
+ *            caller's stream from a private memory pool of the library (which
+ *            keeps up to 64 MiB reserved between calls) and released on the
+ *            same stream: here that of the split path (FK_PATH_SPLIT: very
+ *            long rows, few of them), a few KiB to at most 8 MiB, and in
+ *            fk_q8.h those named there.  fk_softmax_rows_ws (and the _ws forms
+ *            of fk_q8.h) take a caller-provided workspace instead and allocate
+ *            nothing.  Making the pool, at the first workspace, does not
+ *            disturb a stream capture.
  * Layout:    contiguous; softmax rows are row-major with row stride = cols.
  * Streams:   `stream` is a cudaStream_t passed as void* (NULL = the legacy
  *            default stream).  Calls are asynchronous: the kernel is enqueued

@@ -17,8 +17,9 @@
 // The product is bound by reading B once while m is below about 250 (B at
 // 6.5 TB/s against 2 m ops a byte at 3.4 POP/s), by the tensor cores above.
 // Measured on B200 in a captured chain (int8 to bf16): 1 x 16384 x 4096 13.3
-// us (5.0 TB/s of B; alone 10.3 at the copy's rate, the rest is the start and
-// the last blocks), 48 x 32001 x 4096 to fp32 24 us (5.7 TB/s).
+// us with B from HBM each time (5.0 TB/s; alone 10.3 at the copy's rate, the
+// rest is the start and the last blocks), 10.0 with the same B call after
+// call, which L2 holds; 48 x 32001 x 4096 to fp32 25 us (5.5 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -396,8 +397,9 @@ cudaError_t launch_matmul_q8(const MatmulQ8Args& p, void* ws, int sm_count, cuda
     c.k = round16(p.k);
   }
   // Past 64 tokens the pairs of SMs win (128 tokens, 4096 x 4096: 10.9 us
-  // against 12.6 with 128-token tiles here); at 64 and below these kernels do
-  // (64 tokens, 4096 x 4096: 8.5 against 10.9; 16384 x 4096 17.4 against 16.2).
+  // against 12.6 with 128-token tiles here).  At 64 and below it depends on the
+  // channels: 64 tokens of 4096 x 4096 took 8.5 here against 10.9, of 16384 x
+  // 4096 17.4 against 16.2, and the few channels decide the trade.
   if (p.m > kMaxTokens) return mm::launch_pair(c);
   return p.dtype == FK_I8 ? launch_type<FK_I8>(c) : launch_type<FK_E4M3>(c);
 }

@@ -117,8 +117,8 @@ __device__ __forceinline__ float max_words(float m, const uint4& w) {
 
 // One team per row (fk_q8_rows.cuh): read, activation, largest magnitude,
 // codes.  Bound by HBM without GELU; measured on B200: 16384 x 4096 bf16 to
-// e4m3 31.6 us (6.4 TB/s), through the tanh form 37.5 (two MUFU operations a
-// value take 30), through the erf form 62; 8192 x 8192 fp32 50 / 53 / 64.
+// e4m3 30.9 us (6.5 TB/s), through the tanh form 37.7 (two MUFU operations a
+// value take 30), through the erf form 64; 8192 x 8192 fp32 49 / 52 / 64.
 // MAXT, MINB as in fk_rmsnorm.cu.
 template <typename T, int OUT, int EPI, int EPT, bool ALIGNED, int LANES, int MAXT, int MINB, int CL = 1>
 __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_constant__ QuantizeArgs a) {
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_row_kernel(const __grid_c
 // left unrounded, v (Q / max), 80; and 93 with a reciprocal for each value,
 // one read a warp of the row's maxima and the scale applied to single values),
 // 138 through the erf form (26 instructions a value: issue).  The tanh form's
-// rest: MUFU, with 1.5 operations a value at least 46 us, and issue, at 16
-// instructions a value 60, in turns between barriers.
+// rest: MUFU, with 1.5 operations a value at least 46 us, and issue, at 15
+// instructions a value 56, in turns between barriers.
 // Rows whose largest value does not decide the scale (all below about 0.28)
 // take GELU of their packed values twice: 159 and 230 us (rows of 0.05
 // deviation; 553 and 617 when they were read again, value by value).
@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(MAXT, MINB) quantize_walk_kernel(const __grid_
 
 // One 512-thread block per row, which reads the row twice: the largest
 // magnitude, then the codes.  Any length and alignment; value by value, for
-// rows past 131072 columns (2048 x 49152 bf16 to e4m3: 128 us).
+// rows past 131072 columns (1024 x 140000 bf16 to e4m3: 339 us; 960 x 131072 in
+// clusters 130).
 template <typename T, int OUT, int EPI>
 __global__ void __launch_bounds__(kStreamThreads) quantize_stream_kernel(QuantizeArgs a) {
   __shared__ float2 red[kStreamThreads / 32];
@@ -323,8 +324,9 @@ cudaError_t launch_rows(const QuantizeArgs& a, cudaStream_t s) {
   if constexpr (sizeof(T) == 2 && EPI != FK_EPILOGUE_NONE) {
     // two blocks of 512 threads to a row compute one row while another loads
     // (4096 rows, tanh form, us against one block of 1024: 20000 columns 67
-    // and 92, 24576 95 and 103, 32768 113 and 130; without GELU, 32768: 89
-    // and 87)
+    // and 92, 24576 95 and 103, 32768 113 and 130, before codes were those of
+    // the rounded quotient, with which they take 70, 97 and 116; without GELU,
+    // 32768: 89 and 87)
     if (a.cols <= kRowMaxCols) {
       const RowLaunch c = cluster_launch(a.rows, a.cols, 2);
       return launch_overlapped(quantize_row_kernel<T, OUT, EPI, 32, ALIGNED, 0, 512, 2, 2>, c.grid, c.threads, 0, 2, s, a);

@@ -22,9 +22,9 @@ constexpr size_t kMaxGrid = 0x7fffffffu;
 
 // One team per row: it is read, kept, reduced and written (fk_q8_rows.cuh).
 // Bound by HBM; measured on B200, event overhead taken off: 16384 x 4096
-// bf16 + residual to e4m3 and h 77 us (6.1 TB/s), to bf16 81 (6.6 TB/s), the
-// same in fp32 158 (6.8 TB/s); 4096 x 16384 bf16 to e4m3 85; one row of 4096
-// 2.2 us.  Clusters that share a row, and 16 values a thread in place of 32,
+// bf16 + residual to e4m3 and h 73 us (6.4 TB/s), to bf16 82 (6.6 TB/s), the
+// same in fp32 159 (6.8 TB/s); 4096 x 16384 bf16 to e4m3 77; one row of 4096
+// 2.7 us.  Clusters that share a row, and 16 values a thread in place of 32,
 // were slower.
 // MAXT, MINB: threads and blocks per SM the registers are sized for (64 a
 // thread for 1024 threads on an SM).
@@ -200,8 +200,8 @@ cudaError_t launch_rows(const RmsnormArgs& a, cudaStream_t s) {
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 512, 2>, l.grid, l.threads, 0, 1, s, a);
   if (a.cols <= kRowMaxCols)
     return launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 1024, 1>, l.grid, l.threads, 0, 1, s, a);
-  // 4 or 8 blocks of 512 threads (1024 x 65536 bf16 + residual to bf16 108 us,
-  // 1024 x 131072 237; 2 or 4 of 1024: 115 and 265)
+  // 4 or 8 blocks of 512 threads (1024 x 65536 bf16 + residual to bf16 104 us,
+  // 1024 x 131072 236; 2 or 4 of 1024: 115 and 265)
   const int cl = a.cols <= kRowClusterCols / 2 ? 4 : 8;
   const RowLaunch c = cluster_launch(a.rows, a.cols, cl);
   return cl == 4 ? launch_overlapped(rmsnorm_row_kernel<T, OUT, 32, ALIGNED, 0, 512, 2, 4>, c.grid, c.threads, 0, 4, s, a)
