@@ -126,6 +126,47 @@ PFN_attributes attributes_fn() {
   return fn;
 }
 
+// What the driver says of an address: the range it belongs to (an allocation;
+// for virtual memory the whole reservation, mapped or not) and the piece of it
+// that is mapped around the address.
+struct Extent {
+  unsigned type = 0;
+  int owner = -1;
+  CUdeviceptr range = 0, piece = 0;
+  size_t range_size = 0, piece_size = 0;
+};
+bool extent_of(uintptr_t at, Extent* e) {
+  PFN_attributes f = attributes_fn();
+  if (f == nullptr) return false;
+  CUpointer_attribute what[6] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE,       CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                 CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,  CU_POINTER_ATTRIBUTE_RANGE_SIZE,
+                                 CU_POINTER_ATTRIBUTE_MAPPING_BASE_ADDR, CU_POINTER_ATTRIBUTE_MAPPING_SIZE};
+  void* into[6] = {&e->type, &e->owner, &e->range, &e->range_size, &e->piece, &e->piece_size};
+  return f(6, what, into, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS;
+}
+bool within(uintptr_t at, size_t bytes, CUdeviceptr base, size_t size) {
+  return base != 0 && at >= base && at - base <= size && bytes <= size - (at - base);
+}
+
+// Is [lo, lo + bytes) device memory that is mapped throughout?  One
+// allocation, or one reservation of virtual memory mapped in pieces
+// (allocators that grow a segment in place map it so).  Memory whose extent
+// cannot be established is not accepted.
+bool mapped_span(uintptr_t lo, size_t bytes) {
+  PFN_addr_range f = addr_range_fn();
+  if (f == nullptr) return true;
+  Extent e;
+  const bool known = extent_of(lo, &e);
+  for (uintptr_t at = lo;;) {
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    if (f(&base, &size, static_cast<CUdeviceptr>(at)) != CUDA_SUCCESS || at < base || at - base >= size) return false;
+    if (lo + bytes <= base + size) return true;
+    if (!known || !within(lo, bytes, e.range, e.range_size)) return false;
+    at = base + size;
+  }
+}
+
 // Is [p, p + bytes) memory the current device `dev` may access?
 fk_status check_pointer(const void* p, size_t bytes, int dev) {
   cudaPointerAttributes a;
@@ -146,16 +187,8 @@ fk_status check_pointer(const void* p, size_t bytes, int dev) {
     default:  // unregistered (pageable) host memory
       return FK_ERR_INVALID_ARG;
   }
-  if (a.type == cudaMemoryTypeDevice) {
-    if (PFN_addr_range f = addr_range_fn()) {
-      CUdeviceptr base = 0;
-      size_t size = 0;
-      // device memory whose extent cannot be established is not accepted
-      if (f(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return FK_ERR_INVALID_ARG;
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-      if (lo < base || lo - base > size || bytes > size - (lo - base)) return FK_ERR_INVALID_ARG;
-    }
-  }
+  if (a.type == cudaMemoryTypeDevice && !mapped_span(reinterpret_cast<uintptr_t>(p), bytes))
+    return FK_ERR_INVALID_ARG;
   return FK_OK;
 }
 
@@ -205,19 +238,11 @@ fk_status validate_span(const void* p, size_t bytes, size_t align) {
   if (info == nullptr || !info->ok || info->major != 10 || info->minor != 0) return FK_ERR_UNSUPPORTED_DEVICE;
   // device memory, the usual case, in one driver call; anything else through
   // check_pointer
-  if (PFN_attributes f = attributes_fn()) {
-    CUdeviceptr base = 0;
-    size_t size = 0;
-    unsigned type = 0;
-    int owner = -1;
-    CUpointer_attribute what[4] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
-                                   CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
-    void* into[4] = {&type, &owner, &base, &size};
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    if (f(4, what, into, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE &&
-        owner == dev && base != 0 && at >= base && at - base <= size && bytes <= size - (at - base))
-      return FK_OK;
-  }
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  Extent e;
+  if (extent_of(at, &e) && e.type == CU_MEMORYTYPE_DEVICE && e.owner == dev &&
+      within(at, bytes, e.range, e.range_size) && within(at, bytes, e.piece, e.piece_size))
+    return FK_OK;
   return check_pointer(p, bytes, dev);
 }
 

@@ -12,7 +12,7 @@
 namespace fk {
 
 // Is [p, p + bytes) memory that the current device may access, wholly inside
-// one allocation?  (p not NULL, aligned to `align`; also checks that the
+// one allocation (or the mapped part of one reservation)?  (p not NULL, aligned to `align`; also checks that the
 // device is a B200.)
 fk_status validate_span(const void* p, size_t bytes, size_t align);
 
