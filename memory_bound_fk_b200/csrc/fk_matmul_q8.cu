@@ -55,6 +55,7 @@ struct SplitShape {
   static constexpr int kStages = TN >= 64 ? 3 : TN >= 32 ? 4 : 5;
   static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kRedBytes;
   static constexpr uint32_t kTmemCols = TN < 32 ? 32 : TN;
+  static_assert(kSmem >= mm::kSplitSmemLeast, "a pair of SMs would fit beside");
 };
 
 template <int Q8, int TN, int SPLIT, typename T, int EPI>

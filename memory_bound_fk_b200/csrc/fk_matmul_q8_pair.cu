@@ -43,6 +43,7 @@ struct Shape {
   static constexpr uint32_t kStageBytes = kChanBytes + TOK / 2 * kKBlock;
   static constexpr int kStages = TOK == 256 ? 6 : 8;
   static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+  static_assert(kSmem + kSplitSmemLeast > kSmemOfSm, "clusters for few tokens would fit beside");
 };
 // Tiles go to pairs in groups of this many channel tiles by all token tiles,
 // channels fastest, so that concurrent pairs share operands through L2.

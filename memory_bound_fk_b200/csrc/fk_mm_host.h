@@ -17,6 +17,12 @@ constexpr int kKBlock = 128;  // codes of k per stage (one swizzled row)
 // takes 0.3 us alone).
 constexpr uint64_t kWaitNs = 1000000000ull, kStepNs = 2000;
 
+// Shared memory that a block of the kernels for few tokens takes at the least.
+// A pair of SMs takes tensor memory on both at once: it must not find another
+// cluster's block there whose fellow waits for columns that the pair holds.
+// No two such blocks fit an SM together.
+constexpr unsigned kSmemOfSm = 228 * 1024, kSplitSmemLeast = 96 * 1024;
+
 struct Params {
   const float* sa;
   const float* sb;
