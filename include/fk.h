@@ -27,8 +27,10 @@
  * ---------------------------------------
  * Memory:    every pointer is caller-owned memory that the current CUDA
  *            device can access (cudaMalloc / torch tensors, managed or
- *            mapped pinned host memory).  Pageable host memory is rejected
- *            (FK_ERR_INVALID_ARG).  libfk holds no handles and keeps no state
+ *            mapped pinned host memory), one allocation or the mapped pieces
+ *            of one reservation of virtual memory.  Pageable host memory and
+ *            spans past what is mapped are rejected (FK_ERR_INVALID_ARG).
+ *            libfk holds no handles and keeps no state
  *            besides a per-device properties cache and memory pool.  The only
  *            allocations it makes are workspaces, taken stream-ordered on the
  *            caller's stream from a private memory pool of the library (which
@@ -78,7 +80,7 @@ extern "C" {
 typedef enum fk_status {
     FK_OK = 0,
     FK_ERR_INVALID_ARG = 1,        /* NULL pointer, bad size/overflow, misalignment, overlap, bad plan */
-    FK_ERR_UNSUPPORTED_DTYPE = 2,  /* dtype is not one of fk_dtype */
+    FK_ERR_UNSUPPORTED_DTYPE = 2,  /* a dtype that the entry point does not take */
     FK_ERR_UNSUPPORTED_DEVICE = 3, /* no CUDA device, or not compute capability 10.0 (sm_100a) */
     FK_ERR_CUDA = 4                /* a CUDA runtime call or the launch failed */
 } fk_status;

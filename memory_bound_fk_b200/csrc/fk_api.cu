@@ -514,7 +514,7 @@ const char* fk_status_string(int status) {
   switch (status) {
     case FK_OK: return "FK_OK: success";
     case FK_ERR_INVALID_ARG: return "FK_ERR_INVALID_ARG: invalid argument (pointer, size, alignment, overlap or plan)";
-    case FK_ERR_UNSUPPORTED_DTYPE: return "FK_ERR_UNSUPPORTED_DTYPE: dtype must be FK_F32 or FK_BF16";
+    case FK_ERR_UNSUPPORTED_DTYPE: return "FK_ERR_UNSUPPORTED_DTYPE: a dtype that this entry point does not take";
     case FK_ERR_UNSUPPORTED_DEVICE: return "FK_ERR_UNSUPPORTED_DEVICE: no CUDA device, or not sm_100 (B200)";
     case FK_ERR_CUDA: return "FK_ERR_CUDA: a CUDA call or kernel launch failed (see fk_last_cuda_error)";
     default: return "unknown fk_status";
