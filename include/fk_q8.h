@@ -103,6 +103,8 @@ FK_API fk_status fk_rmsnorm_rows(const void *x, const void *residual, const floa
  *   dx     [out] rows*cols values of `dtype`; may be dy, h or dres (in place).
  *   dgamma [out] cols fp32 values, or NULL (not computed).  rows == 0 gives 0.
  *   eps    as in the forward call.
+ * The products dy_j gamma_j h_j and their sum over a row have to lie within
+ * fp32's range.
  * Arithmetic in fp32; dgamma is summed in fp32 in an order fixed by the
  * shape and the way the buffers lie (two equal calls give equal bits).  Rows
  * up to 65536 columns are read once.  Longer ones, and rows of buffers that lie
@@ -157,7 +159,8 @@ FK_API fk_status fk_quantize_rows(const void *x, void *q, float *scales, size_t 
  *             for FK_I8 k <= 131071 (the exact 32-bit sum of products of codes
  *             down to -128 cannot overflow).
  *   dtype     FK_I8 (sums exact in 32-bit integers) or FK_E4M3 (sums in fp32
- *             on the tensor cores).
+ *             on the tensor cores, within (k / 32 + 8) 2^-22 of the sum of the
+ *             products' magnitudes).
  *   epilogue  an fk_epilogue applied to the scaled sum in fp32.
  * The sum is converted to fp32, multiplied by a_scales[i] then b_scales[j],
  * bias added, act applied, and rounded once to `out_dtype`.  Two equal calls

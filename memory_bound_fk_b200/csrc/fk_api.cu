@@ -155,14 +155,13 @@ bool within(uintptr_t at, size_t bytes, CUdeviceptr base, size_t size) {
 bool mapped_span(uintptr_t lo, size_t bytes) {
   PFN_addr_range f = addr_range_fn();
   if (f == nullptr) return true;
-  Extent e;
-  const bool known = extent_of(lo, &e);
   for (uintptr_t at = lo;;) {
     CUdeviceptr base = 0;
     size_t size = 0;
     if (f(&base, &size, static_cast<CUdeviceptr>(at)) != CUDA_SUCCESS || at < base || at - base >= size) return false;
     if (lo + bytes <= base + size) return true;
-    if (!known || !within(lo, bytes, e.range, e.range_size)) return false;
+    Extent e;
+    if (at == lo && (!extent_of(lo, &e) || !within(lo, bytes, e.range, e.range_size))) return false;
     at = base + size;
   }
 }
