@@ -12,7 +12,7 @@
 // the way that v / scale takes them in any fp32 arithmetic.  With 1 / scale in
 // two fp32 terms, hi = rounded and lo = hi (1 - scale hi) (the remainder comes
 // out of one fused multiply-add without error), v hi + v lo in one FMA is
-// within 2^-47 of v / scale before its rounding.  One packed instruction a
+// within 2^-46 of v / scale before its rounding.  One packed instruction a
 // pair more than v hi alone; correcting v hi by its own remainder takes two
 // (8192 x 16384 bf16 through GELU to e4m3, against v hi alone: 3.9% and 7.5%
 // more time; without GELU, and in the norm, under 2%).
